@@ -31,7 +31,9 @@ EXPORTED = ("helm_kv_transfer", "helm_kv_transfer_stage", "helm_kv_transfer_path
             "helm_ridge_fit", "helm_ridge_fit_stage", "helm_ridge_workspace_bytes", "helm_kv_workspace_bytes",
             "helm_kv_paged_workspace_bytes", "helm_mapper_check", "helm_paged_check",
             "helm_device_check", "helm_arch_supported", "helm_last_error", "helm_status_string",
-            "helm_abi_version", "helm_kv_transfer_noalloc", "helm_kv_noalloc_max_bytes")
+            "helm_abi_version", "helm_kv_transfer_noalloc", "helm_kv_noalloc_max_bytes",
+            "helm_rope_plan", "helm_rope", "helm_kv8_store", "helm_kv8_attend", "helm_kv8_attend_workspace_bytes",
+            "helm_kv8_weigh", "helm_kv8_evict", "helm_kv8_check", "helm_kv8_evict_check")
 
 
 class HelmError(RuntimeError):
@@ -133,6 +135,7 @@ def lib() -> ctypes.CDLL:
         L.helm_status_string.argtypes = [ctypes.c_int]
         L.helm_abi_version.restype = ctypes.c_int
         L.helm_abi_version.argtypes = []
+        _bind_serving(L)
         _lib = L
     return _lib
 
@@ -491,3 +494,270 @@ def helm_ridge_fit(X, Y, lam: float = 0.01, W=None, b=None, workspace=None, stag
     shape.workspace, shape.workspace_bytes = _workspace_ptr(workspace, X.device)
     _raise(lib().helm_ridge_fit_stage(int(stages), *ptrs, ctypes.byref(shape)))
     return W, b
+
+
+# ------------------------------------------- serving over a transferred cache
+HELM_ROPE_HALF, HELM_ROPE_INTERLEAVED = 0, 1
+HELM_ROPE_PLAIN, HELM_ROPE_LINEAR, HELM_ROPE_NTK, HELM_ROPE_YARN, HELM_ROPE_BANDED = range(5)
+HELM_ROPE_FORWARD, HELM_ROPE_INVERSE, HELM_ROPE_ADJOINT = range(3)
+
+
+class HelmRope(ctypes.Structure):
+    _fields_ = [
+        ("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+        ("layout", ctypes.c_int32), ("scaling", ctypes.c_int32),
+        ("theta", ctypes.c_double), ("factor", ctypes.c_double), ("original_len", ctypes.c_double),
+        ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+        ("low_freq", ctypes.c_double), ("high_freq", ctypes.c_double), ("magnitude", ctypes.c_double),
+        ("planned", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("freq", ctypes.c_double * 128),
+    ]
+
+
+class HelmRopeShape(ctypes.Structure):
+    _fields_ = [
+        ("n_q_heads", ctypes.c_int32), ("n_k_heads", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("mode", ctypes.c_int32), ("n_tokens", ctypes.c_int64),
+        ("q_tok", ctypes.c_int64), ("q_head", ctypes.c_int64), ("k_tok", ctypes.c_int64), ("k_head", ctypes.c_int64),
+        ("out_q_tok", ctypes.c_int64), ("out_q_head", ctypes.c_int64),
+        ("out_k_tok", ctypes.c_int64), ("out_k_head", ctypes.c_int64),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class HelmKv8Shape(ctypes.Structure):
+    _fields_ = [
+        ("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("block_size", ctypes.c_int32), ("n_blocks", ctypes.c_int32),
+        ("n_requests", ctypes.c_int32), ("max_blocks", ctypes.c_int32),
+        ("causal", ctypes.c_int32), ("window", ctypes.c_int32),
+        ("n_tokens", ctypes.c_int64), ("max_kv_len", ctypes.c_int64),
+        ("tok_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+        ("v_tok_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+        ("softmax_scale", ctypes.c_double),
+        ("stream", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class HelmKv8EvictShape(ctypes.Structure):
+    _fields_ = [
+        ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("block_size", ctypes.c_int32),
+        ("n_blocks", ctypes.c_int32), ("n_requests", ctypes.c_int32),
+        ("max_blocks_src", ctypes.c_int32), ("max_blocks_dst", ctypes.c_int32),
+        ("budget", ctypes.c_int32), ("recent", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("max_kv_len", ctypes.c_int64), ("stream", ctypes.c_void_p),
+    ]
+
+
+def _bind_serving(L):
+    vp, P = ctypes.c_void_p, ctypes.POINTER
+    for name, pointers, shape in (("helm_kv8_store", 10, HelmKv8Shape), ("helm_kv8_attend", 10, HelmKv8Shape),
+                                  ("helm_kv8_weigh", 8, HelmKv8Shape), ("helm_kv8_evict", 10, HelmKv8EvictShape)):
+        f = getattr(L, name)
+        f.restype, f.argtypes = ctypes.c_int, [vp] * pointers + [P(shape)]
+    L.helm_rope.restype, L.helm_rope.argtypes = ctypes.c_int, [vp] * 5 + [P(HelmRope), P(HelmRopeShape)]
+    L.helm_rope_plan.restype, L.helm_rope_plan.argtypes = ctypes.c_int, [P(HelmRope)]
+    L.helm_kv8_attend_workspace_bytes.restype = ctypes.c_size_t
+    L.helm_kv8_attend_workspace_bytes.argtypes = [P(HelmKv8Shape)]
+    L.helm_kv8_check.restype, L.helm_kv8_check.argtypes = ctypes.c_int, [P(HelmKv8Shape)] + [vp] * 3
+    L.helm_kv8_evict_check.restype = ctypes.c_int
+    L.helm_kv8_evict_check.argtypes = [P(HelmKv8EvictShape)] + [vp] * 3
+
+
+def _heads_ptr(t, name, dtype, shape):
+    """Address of a [tokens, heads, dim] tensor of any token and head strides
+    whose heads are contiguous; strides come back with it."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must live on the GPU (got {t.device})")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    tok, head, one = t.stride()
+    if one != 1:
+        raise ValueError(f"the values of a head of {name} must be contiguous (strides {t.stride()})")
+    return t.data_ptr(), max(tok, 1), max(head, 1)
+
+
+def make_rope(head_dim: int, theta: float, rot_dim: int = None, layout: int = HELM_ROPE_HALF,
+              scaling: int = HELM_ROPE_PLAIN, factor: float = 1.0, original_len: float = 0.0,
+              beta_fast: float = 32.0, beta_slow: float = 1.0, low_freq: float = 1.0, high_freq: float = 4.0,
+              magnitude: float = 0.0) -> HelmRope:
+    """A planned helm_rope_t (see include/helm_kv.h): keep it from call to call."""
+    r = HelmRope(head_dim=head_dim, rot_dim=head_dim if rot_dim is None else rot_dim, layout=layout, scaling=scaling,
+                 theta=theta, factor=factor, original_len=original_len, beta_fast=beta_fast, beta_slow=beta_slow,
+                 low_freq=low_freq, high_freq=high_freq, magnitude=magnitude)
+    _raise(lib().helm_rope_plan(ctypes.byref(r)))
+    return r
+
+
+def helm_rope(q, k, pos, rope: HelmRope, mode: int = HELM_ROPE_FORWARD, out_q=None, out_k=None):
+    """Rotary positions of q [N, Hq, D] and k [N, H, D] (either may be None)
+    at pos [N] int32, enqueued on torch's current stream.  Outputs are
+    allocated (contiguous) where not given; out_q=q, out_k=k turns in place.
+    Returns (out_q, out_k)."""
+    import torch
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q or k must be given")
+    s = HelmRopeShape(dtype=_dtype_code(x), mode=mode)
+    N, D = x.shape[0], x.shape[2]
+    if D != rope.head_dim:
+        raise ValueError(f"heads of {D} values, but the plan is for head_dim {rope.head_dim}")
+    ptrs = [None, None, None, None]
+    if q is not None:
+        if out_q is None:
+            out_q = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        s.n_q_heads = q.shape[1]
+        ptrs[0], s.q_tok, s.q_head = _heads_ptr(q, "q", x.dtype, (N, q.shape[1], D))
+        ptrs[2], s.out_q_tok, s.out_q_head = _heads_ptr(out_q, "out_q", x.dtype, (N, q.shape[1], D))
+    if k is not None:
+        if out_k is None:
+            out_k = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        s.n_k_heads = k.shape[1]
+        ptrs[1], s.k_tok, s.k_head = _heads_ptr(k, "k", x.dtype, (N, k.shape[1], D))
+        ptrs[3], s.out_k_tok, s.out_k_head = _heads_ptr(out_k, "out_k", x.dtype, (N, k.shape[1], D))
+    s.n_tokens = N
+    s.stream = current_stream_ptr(x.device) or None
+    _raise(lib().helm_rope(ptrs[0], ptrs[1], _dev_ptr(pos, "pos", torch.int32, (N,)), ptrs[2], ptrs[3],
+                           ctypes.byref(rope), ctypes.byref(s)))
+    return out_q, out_k
+
+
+def make_kv8_shape(k_pool, block_table, n_tokens: int, n_q_heads: int = 0, max_kv_len: int = None,
+                   softmax_scale: float = None, causal: bool = True, window: int = 0) -> HelmKv8Shape:
+    """helm_kv8_shape_t from tensor shapes: k_pool [n_blocks, H, B, D],
+    block_table [R, max_blocks].  softmax_scale defaults to D^-0.5, max_kv_len
+    to what the table can hold."""
+    n_blocks, H, B, D = k_pool.shape
+    R, M = block_table.shape
+    return HelmKv8Shape(n_q_heads=n_q_heads, n_kv_heads=H, head_dim=D, block_size=B, n_blocks=n_blocks, n_requests=R,
+                        max_blocks=M, causal=int(causal), window=window, n_tokens=n_tokens,
+                        max_kv_len=M * B if max_kv_len is None else max_kv_len,
+                        softmax_scale=D ** -0.5 if softmax_scale is None else softmax_scale)
+
+
+def _kv8_ptrs(s, k_pool, v_pool, k_scale, v_scale):
+    import torch
+    pool = (s.n_blocks, s.n_kv_heads, s.block_size, s.head_dim)
+    scale = (s.n_blocks, s.n_kv_heads)
+    return [_dev_ptr(k_pool, "k_pool", torch.float8_e4m3fn, pool), _dev_ptr(v_pool, "v_pool", torch.float8_e4m3fn, pool),
+            _dev_ptr(k_scale, "k_scale", torch.float32, scale), _dev_ptr(v_scale, "v_scale", torch.float32, scale)]
+
+
+def _kv8_tables(s, cu_seqlens, lens, block_table, name):
+    import torch
+    R = s.n_requests
+    return [_dev_ptr(cu_seqlens, "cu_seqlens", torch.int32, (R + 1,)), _dev_ptr(lens, name, torch.int32, (R,)),
+            _dev_ptr(block_table, "block_table", torch.int32, (R, s.max_blocks))]
+
+
+def _kv8_weights(s, weights):
+    import torch
+    return _dev_ptr(weights, "weights", torch.float32, (s.n_blocks, s.n_kv_heads, s.block_size))
+
+
+def helm_kv8_store(k, v, cu_seqlens, kv_start, block_table, k_pool, v_pool, k_scale, v_scale, shape: HelmKv8Shape,
+                   weights=None) -> None:
+    """New tokens k, v [n_tokens, H, D] (bf16 or fp32, any token and head
+    strides) into the 8-bit cache, behind each request's kv_start tokens.
+    ``weights``: the accumulated weights, zeroed for the stored tokens."""
+    s = _call_shape(shape, k_pool.device)
+    s.dtype = _dtype_code(k)
+    nhd = (s.n_tokens, s.n_kv_heads, s.head_dim)
+    kp, s.tok_stride, s.head_stride = _heads_ptr(k, "k", k.dtype, nhd)
+    vp, s.v_tok_stride, s.v_head_stride = _heads_ptr(v, "v", k.dtype, nhd)
+    _raise(lib().helm_kv8_store(kp, vp, *_kv8_tables(s, cu_seqlens, kv_start, block_table, "kv_start"),
+                                *_kv8_ptrs(s, k_pool, v_pool, k_scale, v_scale),
+                                None if weights is None else _kv8_weights(s, weights), ctypes.byref(s)))
+
+
+def helm_kv8_attend_workspace_bytes(shape: HelmKv8Shape) -> int:
+    n = int(lib().helm_kv8_attend_workspace_bytes(ctypes.byref(shape)))
+    if n == 0:
+        raise HelmError(1, helm_last_error())
+    return n
+
+
+def helm_kv8_attend(q, cu_seqlens, kv_len, block_table, k_pool, v_pool, k_scale, v_scale, shape: HelmKv8Shape,
+                    out=None, lse=None, workspace=None):
+    """Attention of q [n_tokens, Hq, D] bf16 (any token and head strides) over
+    the 8-bit cache.  Returns (out [n_tokens, Hq, D] bf16, lse [n_tokens, Hq]
+    fp32), allocated where not given; so is the workspace
+    (helm_kv8_attend_workspace_bytes)."""
+    import torch
+    s = _call_shape(shape, k_pool.device)
+    s.dtype = HELM_BF16
+    nhd = (s.n_tokens, s.n_q_heads, s.head_dim)
+    qp, s.tok_stride, s.head_stride = _heads_ptr(q, "q", torch.bfloat16, nhd)
+    if out is None:
+        out = torch.empty(nhd, dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty(nhd[:2], dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = _own_workspace(helm_kv8_attend_workspace_bytes(s), q.device, s.stream)
+    s.workspace, s.workspace_bytes = _workspace_ptr(workspace, q.device)
+    _raise(lib().helm_kv8_attend(qp, *_kv8_tables(s, cu_seqlens, kv_len, block_table, "kv_len"),
+                                 *_kv8_ptrs(s, k_pool, v_pool, k_scale, v_scale),
+                                 _dev_ptr(out, "out", torch.bfloat16, nhd), _dev_ptr(lse, "lse", torch.float32, nhd[:2]),
+                                 ctypes.byref(s)))
+    return out, lse
+
+
+def helm_kv8_weigh(q, lse, cu_seqlens, kv_len, block_table, k_pool, k_scale, weights, shape: HelmKv8Shape) -> None:
+    """Adds to weights [n_blocks, H, B] the softmax weight that these queries
+    give each cached token; lse as helm_kv8_attend returned it."""
+    import torch
+    s = _call_shape(shape, k_pool.device)
+    s.dtype = HELM_BF16
+    nhd = (s.n_tokens, s.n_q_heads, s.head_dim)
+    qp, s.tok_stride, s.head_stride = _heads_ptr(q, "q", torch.bfloat16, nhd)
+    kp, _, ks, _ = _kv8_ptrs(s, k_pool, k_pool, k_scale, k_scale)
+    _raise(lib().helm_kv8_weigh(qp, _dev_ptr(lse, "lse", torch.float32, nhd[:2]),
+                                *_kv8_tables(s, cu_seqlens, kv_len, block_table, "kv_len"), kp, ks,
+                                _kv8_weights(s, weights), ctypes.byref(s)))
+
+
+def make_kv8_evict_shape(k_pool, src_block_table, dst_block_table, budget: int, recent: int,
+                         max_kv_len: int = None) -> HelmKv8EvictShape:
+    """helm_kv8_evict_shape_t from tensor shapes."""
+    n_blocks, H, B, D = k_pool.shape
+    R, M = src_block_table.shape
+    return HelmKv8EvictShape(n_kv_heads=H, head_dim=D, block_size=B, n_blocks=n_blocks, n_requests=R,
+                             max_blocks_src=M, max_blocks_dst=dst_block_table.shape[1], budget=budget, recent=recent,
+                             max_kv_len=M * B if max_kv_len is None else max_kv_len)
+
+
+def helm_kv8_evict(weights, kv_len, src_block_table, dst_block_table, k_pool, v_pool, k_scale, v_scale,
+                   shape: HelmKv8EvictShape, kept=None, new_len=None):
+    """Keeps each request's most weighted and most recent tokens, per KV head,
+    copied in order into the blocks of dst_block_table (weights too).  Returns
+    (kept [R, H, budget] int32, new_len [R] int32)."""
+    import torch
+    s = _call_shape(shape, k_pool.device)
+    R, H = s.n_requests, s.n_kv_heads
+    if kept is None:
+        kept = torch.empty((R, H, s.budget), dtype=torch.int32, device=k_pool.device)
+    if new_len is None:
+        new_len = torch.empty((R,), dtype=torch.int32, device=k_pool.device)
+    _raise(lib().helm_kv8_evict(_dev_ptr(kv_len, "kv_len", torch.int32, (R,)),
+                                _dev_ptr(src_block_table, "src_block_table", torch.int32, (R, s.max_blocks_src)),
+                                _dev_ptr(dst_block_table, "dst_block_table", torch.int32, (R, s.max_blocks_dst)),
+                                *_kv8_ptrs(s, k_pool, v_pool, k_scale, v_scale), _kv8_weights(s, weights),
+                                _dev_ptr(kept, "kept", torch.int32, (R, H, s.budget)),
+                                _dev_ptr(new_len, "new_len", torch.int32, (R,)), ctypes.byref(s)))
+    return kept, new_len
+
+
+def helm_kv8_check(shape: HelmKv8Shape, cu_seqlens_host, kv_len_host, block_table_host) -> int:
+    (a, ka), (b, kb), (c, kc) = (_host_i32(x) for x in (cu_seqlens_host, kv_len_host, block_table_host))
+    return int(lib().helm_kv8_check(ctypes.byref(shape), a, b, c))
+
+
+def helm_kv8_evict_check(shape: HelmKv8EvictShape, kv_len_host, src_block_table_host, dst_block_table_host) -> int:
+    (a, ka), (b, kb), (c, kc) = (_host_i32(x) for x in (kv_len_host, src_block_table_host, dst_block_table_host))
+    return int(lib().helm_kv8_evict_check(ctypes.byref(shape), a, b, c))

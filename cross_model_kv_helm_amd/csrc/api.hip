@@ -11,11 +11,14 @@
 #include <vector>
 
 #include "../../include/helm_kv.h"
+#include "entry.hpp"
 #include "internal.hpp"
 
 namespace {
-
 thread_local char g_err[512] = "";
+}
+
+namespace helm::entry {
 
 int fail(int status, const char* fmt, ...) {
   std::va_list ap;
@@ -26,9 +29,6 @@ int fail(int status, const char* fmt, ...) {
 }
 
 void clear_error() { g_err[0] = '\0'; }
-
-constexpr size_t kAlign = 256;
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 // Multiplies non-negative factors; returns false on int64 overflow.
 bool mul_ok(int64_t& acc, int64_t f) {
@@ -43,6 +43,12 @@ bool overlaps(const void* a, int64_t na, const void* b, int64_t nb) {
   const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
   return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
 }
+
+}  // namespace helm::entry
+
+using namespace helm::entry;
+
+namespace {
 
 // Fields common to both shapes.
 struct Common {
@@ -106,6 +112,10 @@ bool workspace_layout(int64_t n_tok, int32_t D, bool paged, Workspace& w) {
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_dev_state[kMaxDevices];   // 0 unknown, 1 ok, 2 wrong arch
 
+}  // namespace
+
+namespace helm::entry {
+
 int device_gate(int device) {
   int count = 0;
   hipError_t e = hipGetDeviceCount(&count);
@@ -140,6 +150,10 @@ int launch_status(hipError_t e, const char* what) {
   if (e == hipSuccess) return HELM_OK;
   return fail(HELM_E_LAUNCH, "%s: %s", what, hipGetErrorString(e));
 }
+
+}  // namespace helm::entry
+
+namespace {
 
 int run_transfer(helm::XferArgs& a, int32_t dtype, const int32_t* src_pos, const int32_t* tgt_pos,
                  double th_s, double th_t, hipStream_t stream, int stages = HELM_STAGE_ALL) {

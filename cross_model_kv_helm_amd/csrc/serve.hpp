@@ -1,0 +1,157 @@
+// serve.hpp — kernel arguments of the calls that serve over a transferred
+// cache (rotary positions, the 8-bit paged cache); include/helm_kv.h states
+// what each computes.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "internal.hpp"
+
+namespace helm {
+
+constexpr int kRopePairs = 128;
+struct RopeTurns {
+  double turn[kRopePairs];   // turns per position of each pair
+};
+struct RopeArgs {
+  const void* q;
+  const void* k;
+  void* out_q;
+  void* out_k;
+  const int32_t* pos;
+  int64_t n_tok;
+  int64_t q_tok, q_head, k_tok, k_head, oq_tok, oq_head, ok_tok, ok_head;   // element strides
+  int32_t n_q, n_k, D, pairs;
+  float mag, sign;           // what cos and sin are multiplied by; -1 turns back
+  int32_t tok, heads_per;    // set at the launch
+};
+hipError_t launch_rope(const RopeArgs& a, const RopeTurns& f, bool interleaved, Dtype dt, hipStream_t stream);
+
+// The 8-bit paged cache of one layer: codes [n_blocks, H, B, D], scales
+// [n_blocks, H], block table [R, max_blocks].
+struct Kv8Cache {
+  uint8_t* k_pool;
+  uint8_t* v_pool;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* table;
+  int32_t H, D, B, n_blocks, R, max_blocks;
+  int32_t max_len;           // tokens past it (or past max_blocks * B) are absent
+  // page of a token: t / B = umulhi(t / 16, page_magic), see page_magic_of
+  uint32_t page_magic;
+};
+// floor(n / d) = umulhi(n, magic) for n < 2^28 and 2 <= d <= 16: the error of
+// magic = ceil(2^32 / d) is below d, so n * error < 2^32.  d = 1 gives 0: the
+// quotient is n itself.
+inline uint32_t page_magic_of(int32_t block_size) {
+  const uint64_t d = (uint64_t)block_size / 16;
+  return d == 1 ? 0u : (uint32_t)(((uint64_t(1) << 32) + d - 1) / d);
+}
+
+struct Kv8StoreArgs {
+  Kv8Cache c;
+  const void* k;
+  const void* v;
+  int64_t k_tok, k_head, v_tok, v_head;
+  const int32_t* cu;
+  const int32_t* start;
+  float* weights;            // or nullptr
+  int64_t n_tok;
+};
+hipError_t launch_kv8_store(const Kv8StoreArgs& a, Dtype dt, hipStream_t stream);
+
+struct Kv8AttendArgs {
+  Kv8Cache c;
+  const uint16_t* q;
+  int64_t q_tok, q_head;
+  const int32_t* cu;
+  const int32_t* kv_len;
+  uint16_t* out;
+  float* lse;                // written by attend, read by weigh
+  float* weights;            // weigh
+  float* part;               // workspace of a split context: [splits][n_tok * Hq] (m, l), then [..][D] sums
+  int64_t n_tok;
+  int32_t Hq, G, causal, window;
+  float scale_log2;          // softmax_scale * log2(e)
+  int32_t splits, chunk;     // pieces of the context and tokens in each
+};
+// The pieces that a context is split into: a function of the shape alone.
+void kv8_attend_split(Kv8AttendArgs& a);
+size_t kv8_attend_workspace(const Kv8AttendArgs& a);
+hipError_t launch_kv8_attend(const Kv8AttendArgs& a, hipStream_t stream);
+hipError_t launch_kv8_weigh(const Kv8AttendArgs& a, hipStream_t stream);
+
+struct Kv8EvictArgs {
+  Kv8Cache c;                // table = src
+  const int32_t* dst;
+  int32_t max_dst;
+  const int32_t* kv_len;
+  float* weights;
+  int32_t* kept;
+  int32_t* new_len;
+  int32_t budget, recent;
+};
+hipError_t launch_kv8_evict(const Kv8EvictArgs& a, hipStream_t stream);
+
+// ---- device helpers ------------------------------------------------------
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// cu_seqlens entry, kept inside the packed tokens whatever it says.
+__device__ __forceinline__ int64_t cu_at(const int32_t* cu, int r, int64_t n_tok) {
+  const int64_t x = cu[r];
+  return x < 0 ? 0 : x > n_tok ? n_tok : x;
+}
+
+// A ragged batch is given work items without the host reading its lengths:
+// request r owns the items from base(r) = floor(cu[r] * num / den) + slack * r
+// up to base(r + 1), at least floor(n * num / den) + slack of them.  Returns
+// the owner of `item` and sets its base.  Uniform over the wave.
+__device__ __forceinline__ int owner_of(const int32_t* cu, int R, int64_t n_tok, int num, int den, int slack,
+                                        int64_t item, int64_t& base) {
+  const int lane = threadIdx.x & 63;
+  int count = 0;
+  for (int r0 = 0; r0 < R; r0 += 64) {
+    const int r = r0 + lane;
+    const bool under = r < R && cu_at(cu, r, n_tok) * num / den + (int64_t)slack * r <= item;
+    const int c = __popcll(__ballot(under));
+    count += c;
+    if (c < 64) break;
+  }
+  const int r = __builtin_amdgcn_readfirstlane(max(count - 1, 0));
+  base = cu_at(cu, r, n_tok) * num / den + (int64_t)slack * r;
+  return r;
+}
+
+// Smallest power of two 2^e, -120 <= e <= 120, with amax <= 448 * 2^e.
+__device__ __forceinline__ float kv8_scale_of(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);   // 448 = 1.75 * 2^8
+  e = min(max(e, -120), 120);
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+// |x| for the scale: infinities and NaN do not count.
+__device__ __forceinline__ float kv8_size(float x) {
+  const float a = fabsf(x);
+  return a <= 3.402823466e38f ? a : 0.0f;
+}
+// Into +-448; NaN stays.
+__device__ __forceinline__ float kv8_clamp(float x) {
+  return x != x ? x : fminf(fmaxf(x, -448.0f), 448.0f);
+}
+__device__ __forceinline__ uint32_t kv8_encode4(float a, float b, float c, float d) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(kv8_clamp(a), kv8_clamp(b), 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(kv8_clamp(c), kv8_clamp(d), w, true);
+}
+__device__ __forceinline__ f32x4 kv8_decode4(uint32_t w) {
+  const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
+  const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+  return f32x4{lo[0], lo[1], hi[0], hi[1]};
+}
+
+}  // namespace helm

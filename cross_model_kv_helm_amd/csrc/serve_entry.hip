@@ -1,0 +1,518 @@
+// serve_entry.hip — the C entry points that serve over a transferred cache
+// (include/helm_kv.h, second part): host-side validation, workspace sizes and
+// dispatch.  Every check runs before anything is enqueued.
+#include <cmath>
+#include <new>
+#include <vector>
+
+#include "../../include/helm_kv.h"
+#include "entry.hpp"
+#include "serve.hpp"
+
+using namespace helm::entry;
+
+namespace {
+
+constexpr double kTwoPi = 6.283185307179586476925286766559;
+constexpr int64_t kMaxContext = int64_t(1) << 30;
+
+struct Range {
+  const void* p;
+  int64_t bytes;
+  const char* name;
+};
+
+// No output may share a byte with an input or another output.
+int check_alias(const Range* outs, int n_out, const Range* ins, int n_in) {
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = 0; j < n_in; ++j)
+      if (overlaps(outs[i].p, outs[i].bytes, ins[j].p, ins[j].bytes))
+        return fail(HELM_E_ALIAS, "%s overlaps %s", outs[i].name, ins[j].name);
+    for (int j = 0; j < i; ++j)
+      if (overlaps(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes))
+        return fail(HELM_E_ALIAS, "%s overlaps %s", outs[i].name, outs[j].name);
+  }
+  return HELM_OK;
+}
+
+// Bytes from the first to the last value of [tokens, heads, D] with these
+// element strides; -1 where they overflow or are not positive.
+int64_t span_bytes(int64_t tokens, int64_t heads, int64_t D, int64_t tok, int64_t head, int64_t elem) {
+  if (tok < 1 || head < 1) return -1;
+  int64_t a = tokens - 1, b = heads - 1;
+  if (!mul_ok(a, tok) || !mul_ok(b, head)) return -1;
+  if (a > INT64_MAX - b - D) return -1;
+  int64_t n = a + b + D;
+  return mul_ok(n, elem) ? n : -1;
+}
+
+// A strided [tokens, heads, D] operand: where it lies and how its tokens step.
+struct Slices {
+  const void* p;
+  int64_t bytes, tok, row;   // whole span, a token's step and one token's span, in bytes
+};
+// Slices of one fused tensor interleave without sharing a byte: equal steps,
+// and each token's span clear of the other's.
+bool share_bytes(const Slices& a, const Slices& b) {
+  if (!overlaps(a.p, a.bytes, b.p, b.bytes)) return false;
+  if (a.tok != b.tok || a.row > a.tok || b.row > b.tok) return true;
+  const int64_t apart = (int64_t)(uintptr_t)b.p - (int64_t)(uintptr_t)a.p;
+  const int64_t at = (apart % a.tok + a.tok) % a.tok;   // b's token begins here in a's step
+  return at < a.row || at + b.row > a.tok;
+}
+
+// ---- rotary positions ----------------------------------------------------
+int check_rope(const helm_rope_t* r) {
+  if (!r) return fail(HELM_E_INVALID_ARG, "rope is NULL");
+  if (r->head_dim < 2 || r->head_dim > 2 * HELM_ROPE_MAX_PAIRS)
+    return fail(HELM_E_PAIR_SHAPE, "head_dim %d lies outside 2..%d", r->head_dim, 2 * HELM_ROPE_MAX_PAIRS);
+  if (r->rot_dim < 2 || r->rot_dim > r->head_dim || (r->rot_dim & 1))
+    return fail(HELM_E_PAIR_SHAPE, "rot_dim %d must be even and lie in 2..head_dim (%d)", r->rot_dim, r->head_dim);
+  if (r->layout != HELM_ROPE_HALF && r->layout != HELM_ROPE_INTERLEAVED)
+    return fail(HELM_E_INVALID_ARG, "unknown RoPE layout %d", r->layout);
+  if (r->scaling < HELM_ROPE_PLAIN || r->scaling > HELM_ROPE_BANDED)
+    return fail(HELM_E_INVALID_ARG, "unknown RoPE scaling %d", r->scaling);
+  if (!(r->theta > 0.0) || !std::isfinite(r->theta))
+    return fail(HELM_E_INVALID_ARG, "RoPE base must be finite and > 0 (%g)", r->theta);
+  if (r->scaling != HELM_ROPE_PLAIN && (!(r->factor > 0.0) || !std::isfinite(r->factor)))
+    return fail(HELM_E_INVALID_ARG, "RoPE scaling factor must be finite and > 0 (%g)", r->factor);
+  if ((r->scaling == HELM_ROPE_YARN || r->scaling == HELM_ROPE_BANDED) &&
+      (!(r->original_len > 0.0) || !std::isfinite(r->original_len)))
+    return fail(HELM_E_INVALID_ARG, "original_len must be finite and > 0 (%g)", r->original_len);
+  if (r->scaling == HELM_ROPE_YARN) {
+    if (!(r->theta > 1.0)) return fail(HELM_E_INVALID_ARG, "YARN needs a RoPE base > 1 (%g)", r->theta);
+    if (!(r->beta_fast > 0.0) || !(r->beta_slow > 0.0) || !std::isfinite(r->beta_fast) ||
+        !std::isfinite(r->beta_slow))
+      return fail(HELM_E_INVALID_ARG, "beta_fast and beta_slow must be finite and > 0 (%g, %g)", r->beta_fast,
+                  r->beta_slow);
+  }
+  if (r->scaling == HELM_ROPE_BANDED &&
+      (!std::isfinite(r->low_freq) || !std::isfinite(r->high_freq) || !(r->low_freq < r->high_freq)))
+    return fail(HELM_E_INVALID_ARG, "low_freq must lie below high_freq (%g, %g)", r->low_freq, r->high_freq);
+  if (!(r->magnitude >= 0.0) || !std::isfinite(r->magnitude))
+    return fail(HELM_E_INVALID_ARG, "magnitude must be finite and >= 0 (%g)", r->magnitude);
+  return HELM_OK;
+}
+
+// ---- the 8-bit cache ------------------------------------------------------
+int check_cache(int32_t H, int32_t D, int32_t B, int32_t n_blocks, int32_t R, int64_t max_len) {
+  if (H < 1 || H > 65535) return fail(HELM_E_INVALID_ARG, "n_kv_heads=%d must lie in 1..65535", H);
+  if (D != 64 && D != 128) return fail(HELM_E_PAIR_SHAPE, "head_dim %d is not supported (64 or 128)", D);
+  if (B < 16 || B > 256 || B % 16)
+    return fail(HELM_E_INVALID_ARG, "block_size %d must be a multiple of 16 in 16..256", B);
+  if (n_blocks < 1) return fail(HELM_E_INVALID_ARG, "n_blocks=%d must be >= 1", n_blocks);
+  if (R < 1 || R > 32767) return fail(HELM_E_INVALID_ARG, "n_requests=%d must lie in 1..32767", R);
+  if (max_len < 0 || max_len > kMaxContext)
+    return fail(HELM_E_INVALID_ARG, "max_kv_len=%lld must lie in 0..2^30", (long long)max_len);
+  int64_t n = n_blocks;
+  if (!mul_ok(n, H) || !mul_ok(n, (int64_t)B * D)) return fail(HELM_E_INVALID_ARG, "pool size overflows int64");
+  return HELM_OK;
+}
+
+int check_kv8(const helm_kv8_shape_t* s) {
+  if (!s) return fail(HELM_E_INVALID_ARG, "shape is NULL");
+  int rc = check_cache(s->n_kv_heads, s->head_dim, s->block_size, s->n_blocks, s->n_requests, s->max_kv_len);
+  if (rc != HELM_OK) return rc;
+  if (s->max_blocks < 1) return fail(HELM_E_INVALID_ARG, "max_blocks=%d must be >= 1", s->max_blocks);
+  if (s->n_tokens < 0 || s->n_tokens > 0x7fffffffLL)
+    return fail(HELM_E_INVALID_ARG, "n_tokens=%lld must lie in 0..2^31-1", (long long)s->n_tokens);
+  return HELM_OK;
+}
+
+int check_queries(const helm_kv8_shape_t* s) {
+  if (s->n_q_heads < 1 || s->n_q_heads % s->n_kv_heads)
+    return fail(HELM_E_INVALID_ARG, "n_q_heads=%d must be a positive multiple of n_kv_heads=%d", s->n_q_heads,
+                s->n_kv_heads);
+  if (s->dtype != HELM_BF16)
+    return fail(HELM_E_DTYPE, "queries over the 8-bit cache are bf16 (dtype %d)", s->dtype);
+  if (s->causal != 0 && s->causal != 1) return fail(HELM_E_INVALID_ARG, "causal=%d must be 0 or 1", s->causal);
+  if (s->window < 0 || (s->window > 0 && !s->causal))
+    return fail(HELM_E_INVALID_ARG, "window=%d must be >= 0, and 0 without causal", s->window);
+  if (!std::isfinite(s->softmax_scale)) return fail(HELM_E_INVALID_ARG, "softmax_scale must be finite");
+  int64_t rows = s->n_tokens;
+  if (!mul_ok(rows, s->n_q_heads) || rows > 0x7fffffffLL)
+    return fail(HELM_E_INVALID_ARG, "n_tokens * n_q_heads exceeds 2^31-1");
+  return HELM_OK;
+}
+
+helm::Kv8Cache cache_of(const helm_kv8_shape_t* s, const void* k_pool, const void* v_pool, const float* k_scale,
+                        const float* v_scale, const int32_t* table) {
+  helm::Kv8Cache c{};
+  c.k_pool = (uint8_t*)k_pool; c.v_pool = (uint8_t*)v_pool;
+  c.k_scale = (float*)k_scale; c.v_scale = (float*)v_scale;
+  c.table = table;
+  c.H = s->n_kv_heads; c.D = s->head_dim; c.B = s->block_size; c.n_blocks = s->n_blocks;
+  c.R = s->n_requests; c.max_blocks = s->max_blocks;
+  c.max_len = (int32_t)s->max_kv_len;
+  c.page_magic = helm::page_magic_of(c.B);
+  return c;
+}
+
+helm::Kv8AttendArgs attend_args(const helm_kv8_shape_t* s) {
+  helm::Kv8AttendArgs a{};
+  a.c = cache_of(s, nullptr, nullptr, nullptr, nullptr, nullptr);
+  a.n_tok = s->n_tokens;
+  a.Hq = s->n_q_heads;
+  a.G = s->n_q_heads / s->n_kv_heads;
+  a.causal = s->causal;
+  a.window = s->window;
+  a.scale_log2 = (float)(s->softmax_scale * 1.4426950408889634);
+  a.q_tok = s->tok_stride;
+  a.q_head = s->head_stride;
+  // no request can hold more than its table's pages
+  const int64_t room = (int64_t)s->max_blocks * s->block_size;
+  if (room < a.c.max_len) a.c.max_len = (int32_t)room;
+  helm::kv8_attend_split(a);
+  return a;
+}
+
+int check_aligned(const void* p, const char* name, size_t to) {
+  return (uintptr_t)p % to ? fail(HELM_E_INVALID_ARG, "%s is not %zu-byte aligned", name, to) : HELM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int helm_rope_plan(helm_rope_t* r) {
+  clear_error();
+  int rc = check_rope(r);
+  if (rc != HELM_OK) return rc;
+  const int rot = r->rot_dim, P = rot / 2;
+  const double f = r->factor, L = r->original_len;
+  double theta = r->theta;
+  if (r->scaling == HELM_ROPE_NTK && rot > 2) theta *= std::pow(f, (double)rot / (rot - 2));
+  double lo = 0.0, hi = 0.0;
+  if (r->scaling == HELM_ROPE_YARN) {
+    const double per = rot / (2.0 * std::log(theta));
+    lo = std::fmax(0.0, std::floor(per * std::log(L / (r->beta_fast * kTwoPi))));
+    hi = std::fmin(rot - 1.0, std::ceil(per * std::log(L / (r->beta_slow * kTwoPi))));
+  }
+  for (int i = 0; i < HELM_ROPE_MAX_PAIRS; ++i) r->freq[i] = 0.0;
+  for (int i = 0; i < P; ++i) {
+    double w = std::pow(theta, -2.0 * i / rot);
+    if (r->scaling == HELM_ROPE_LINEAR) {
+      w /= f;
+    } else if (r->scaling == HELM_ROPE_YARN) {
+      const double ramp = std::fmin(1.0, std::fmax(0.0, (i - lo) / std::fmax(hi - lo, 1e-3)));
+      w *= ramp / f + 1.0 - ramp;
+    } else if (r->scaling == HELM_ROPE_BANDED) {
+      const double turns = L * w / kTwoPi;
+      const double keep =
+          std::fmin(1.0, std::fmax(0.0, (turns - r->low_freq) / (r->high_freq - r->low_freq)));
+      w *= (1.0 - keep) / f + keep;
+    }
+    if (!std::isfinite(w)) return fail(HELM_E_INVALID_ARG, "the RoPE frequency of pair %d is not finite", i);
+    r->freq[i] = w;
+  }
+  if (r->magnitude == 0.0) r->magnitude = r->scaling == HELM_ROPE_YARN ? 0.1 * std::log(f) + 1.0 : 1.0;
+  if (!(r->magnitude > 0.0)) return fail(HELM_E_INVALID_ARG, "the RoPE magnitude %g is not positive", r->magnitude);
+  r->planned = 1;
+  return HELM_OK;
+}
+
+int helm_rope(const void* q, const void* k, const int32_t* pos, void* out_q, void* out_k, const helm_rope_t* r,
+              const helm_rope_shape_t* s) {
+  clear_error();
+  int rc = check_rope(r);
+  if (rc != HELM_OK) return rc;
+  if (r->planned != 1 || !(r->magnitude > 0.0))
+    return fail(HELM_E_INVALID_ARG, "rope has not been through helm_rope_plan");
+  if (!s) return fail(HELM_E_INVALID_ARG, "shape is NULL");
+  if (s->dtype != HELM_BF16 && s->dtype != HELM_F32)
+    return fail(HELM_E_DTYPE, "unknown dtype code %d (HELM_BF16=0, HELM_F32=1)", s->dtype);
+  if (s->mode < HELM_ROPE_FORWARD || s->mode > HELM_ROPE_ADJOINT)
+    return fail(HELM_E_INVALID_ARG, "unknown RoPE mode %d", s->mode);
+  if (s->n_q_heads < 0 || s->n_k_heads < 0 || (int64_t)s->n_q_heads + s->n_k_heads > 65535)
+    return fail(HELM_E_INVALID_ARG, "head counts must be >= 0 and their sum at most 65535 (%d, %d)", s->n_q_heads,
+                s->n_k_heads);
+  if (s->n_tokens < 0 || s->n_tokens > 0x7fffffffLL)
+    return fail(HELM_E_INVALID_ARG, "n_tokens=%lld must lie in 0..2^31-1", (long long)s->n_tokens);
+  if (s->n_tokens == 0 || s->n_q_heads + s->n_k_heads == 0) return HELM_OK;
+  const int64_t e = s->dtype == HELM_BF16 ? 2 : 4;
+  const struct {
+    const void* in;
+    const void* out;
+    int32_t heads;
+    int64_t it, ih, ot, oh;
+    const char *in_name, *out_name;
+  } side[2] = {{q, out_q, s->n_q_heads, s->q_tok, s->q_head, s->out_q_tok, s->out_q_head, "q", "out_q"},
+               {k, out_k, s->n_k_heads, s->k_tok, s->k_head, s->out_k_tok, s->out_k_head, "k", "out_k"}};
+  if (!pos) return fail(HELM_E_INVALID_ARG, "pos is NULL");
+  Slices in[2] = {}, out[2] = {};
+  for (int i = 0; i < 2; ++i) {
+    if (!side[i].heads) continue;
+    if (!side[i].in || !side[i].out) return fail(HELM_E_INVALID_ARG, "%s or %s is NULL", side[i].in_name, side[i].out_name);
+    if ((uintptr_t)side[i].in % e || (uintptr_t)side[i].out % e)
+      return fail(HELM_E_INVALID_ARG, "%s or %s is not aligned to its elements", side[i].in_name, side[i].out_name);
+    const int64_t a = span_bytes(s->n_tokens, side[i].heads, r->head_dim, side[i].it, side[i].ih, e);
+    const int64_t b = span_bytes(s->n_tokens, side[i].heads, r->head_dim, side[i].ot, side[i].oh, e);
+    if (a < 0 || b < 0)
+      return fail(HELM_E_INVALID_ARG, "strides of %s or %s are not positive or overflow", side[i].in_name,
+                  side[i].out_name);
+    in[i] = {side[i].in, a, side[i].it * e, span_bytes(1, side[i].heads, r->head_dim, 1, side[i].ih, e)};
+    out[i] = {side[i].out, b, side[i].ot * e, span_bytes(1, side[i].heads, r->head_dim, 1, side[i].oh, e)};
+  }
+  for (int i = 0; i < 2; ++i) {
+    if (!side[i].heads) continue;
+    if (overlaps(out[i].p, out[i].bytes, pos, s->n_tokens * 4))
+      return fail(HELM_E_ALIAS, "%s overlaps pos", side[i].out_name);
+    for (int j = 0; j < 2; ++j) {
+      const bool own = j == i && side[i].in == side[i].out && side[i].it == side[i].ot && side[i].ih == side[i].oh;
+      if (side[j].heads && !own && share_bytes(out[i], in[j]))
+        return fail(HELM_E_ALIAS, "%s overlaps %s", side[i].out_name, side[j].in_name);
+    }
+  }
+  if (side[0].heads && side[1].heads && share_bytes(out[0], out[1]))
+    return fail(HELM_E_ALIAS, "out_k overlaps out_q");
+  rc = device_gate(-1);
+  if (rc != HELM_OK) return rc;
+
+  helm::RopeArgs a{};
+  a.q = q; a.k = k; a.out_q = out_q; a.out_k = out_k; a.pos = pos;
+  a.n_tok = s->n_tokens;
+  a.q_tok = s->q_tok; a.q_head = s->q_head; a.k_tok = s->k_tok; a.k_head = s->k_head;
+  a.oq_tok = s->out_q_tok; a.oq_head = s->out_q_head; a.ok_tok = s->out_k_tok; a.ok_head = s->out_k_head;
+  a.n_q = s->n_q_heads; a.n_k = s->n_k_heads; a.D = r->head_dim; a.pairs = r->rot_dim / 2;
+  a.mag = (float)(s->mode == HELM_ROPE_INVERSE ? 1.0 / r->magnitude : r->magnitude);
+  a.sign = s->mode == HELM_ROPE_FORWARD ? 1.0f : -1.0f;
+  helm::RopeTurns f;
+  for (int i = 0; i < helm::kRopePairs; ++i) f.turn[i] = i < a.pairs ? r->freq[i] / kTwoPi : 0.0;
+  return launch_status(helm::launch_rope(a, f, r->layout == HELM_ROPE_INTERLEAVED,
+                                         s->dtype == HELM_BF16 ? helm::Dtype::BF16 : helm::Dtype::F32,
+                                         (hipStream_t)s->stream),
+                       "rotary positions launch");
+}
+
+int helm_kv8_store(const void* k, const void* v, const int32_t* cu, const int32_t* start, const int32_t* table,
+                   void* k_pool, void* v_pool, float* k_scale, float* v_scale, float* weights,
+                   const helm_kv8_shape_t* s) {
+  clear_error();
+  int rc = check_kv8(s);
+  if (rc != HELM_OK) return rc;
+  if (s->dtype != HELM_BF16 && s->dtype != HELM_F32)
+    return fail(HELM_E_DTYPE, "unknown dtype code %d (HELM_BF16=0, HELM_F32=1)", s->dtype);
+  if (s->n_tokens == 0) return HELM_OK;
+  if (!k || !v || !cu || !start || !table || !k_pool || !v_pool || !k_scale || !v_scale)
+    return fail(HELM_E_INVALID_ARG, "a tensor pointer is NULL");
+  const int64_t e = s->dtype == HELM_BF16 ? 2 : 4, H = s->n_kv_heads, D = s->head_dim;
+  const int64_t kb = span_bytes(s->n_tokens, H, D, s->tok_stride, s->head_stride, e);
+  const int64_t vb = span_bytes(s->n_tokens, H, D, s->v_tok_stride, s->v_head_stride, e);
+  if (kb < 0 || vb < 0) return fail(HELM_E_INVALID_ARG, "strides of k or v are not positive or overflow");
+  if ((uintptr_t)k % e || (uintptr_t)v % e) return fail(HELM_E_INVALID_ARG, "k or v is not aligned to its elements");
+  if ((rc = check_aligned(k_pool, "k_pool", 16)) || (rc = check_aligned(v_pool, "v_pool", 16))) return rc;
+  const int64_t slabs = (int64_t)s->n_blocks * H, R = s->n_requests;
+  const Range outs[] = {{k_pool, slabs * s->block_size * D, "k_pool"}, {v_pool, slabs * s->block_size * D, "v_pool"},
+                        {k_scale, slabs * 4, "k_scale"}, {v_scale, slabs * 4, "v_scale"},
+                        {weights, slabs * s->block_size * 4, "weights"}};
+  const Range ins[] = {{k, kb, "k"}, {v, vb, "v"}, {cu, (R + 1) * 4, "cu_seqlens"}, {start, R * 4, "kv_start"},
+                       {table, R * s->max_blocks * 4, "block_table"}};
+  if ((rc = check_alias(outs, 5, ins, 5)) != HELM_OK) return rc;
+  rc = device_gate(-1);
+  if (rc != HELM_OK) return rc;
+  helm::Kv8StoreArgs a{};
+  a.c = cache_of(s, k_pool, v_pool, k_scale, v_scale, table);
+  a.k = k; a.v = v; a.cu = cu; a.start = start; a.weights = weights;
+  a.k_tok = s->tok_stride; a.k_head = s->head_stride; a.v_tok = s->v_tok_stride; a.v_head = s->v_head_stride;
+  a.n_tok = s->n_tokens;
+  return launch_status(helm::launch_kv8_store(a, s->dtype == HELM_BF16 ? helm::Dtype::BF16 : helm::Dtype::F32,
+                                              (hipStream_t)s->stream),
+                       "8-bit store launch");
+}
+
+size_t helm_kv8_attend_workspace_bytes(const helm_kv8_shape_t* s) {
+  clear_error();
+  if (check_kv8(s) != HELM_OK || check_queries(s) != HELM_OK) return 0;
+  const size_t n = helm::kv8_attend_workspace(attend_args(s));
+  return n ? align_up(n) : kAlign;
+}
+
+int helm_kv8_attend(const void* q, const int32_t* cu, const int32_t* kv_len, const int32_t* table,
+                    const void* k_pool, const void* v_pool, const float* k_scale, const float* v_scale, void* out,
+                    float* lse, const helm_kv8_shape_t* s) {
+  clear_error();
+  int rc = check_kv8(s);
+  if (rc != HELM_OK || (rc = check_queries(s)) != HELM_OK) return rc;
+  if (s->n_tokens == 0) return HELM_OK;
+  if (!q || !cu || !kv_len || !table || !k_pool || !v_pool || !k_scale || !v_scale || !out || !lse)
+    return fail(HELM_E_INVALID_ARG, "a tensor pointer is NULL");
+  const int64_t D = s->head_dim, R = s->n_requests, slabs = (int64_t)s->n_blocks * s->n_kv_heads;
+  const int64_t qb = span_bytes(s->n_tokens, s->n_q_heads, D, s->tok_stride, s->head_stride, 2);
+  if (qb < 0) return fail(HELM_E_INVALID_ARG, "strides of q are not positive or overflow");
+  if ((rc = check_aligned(q, "q", 2)) || (rc = check_aligned(k_pool, "k_pool", 16)) ||
+      (rc = check_aligned(v_pool, "v_pool", 16)) || (rc = check_aligned(out, "out", 16)))
+    return rc;
+  helm::Kv8AttendArgs a = attend_args(s);
+  const size_t need = helm::kv8_attend_workspace(a);
+  const int64_t rows = s->n_tokens * s->n_q_heads;
+  Range outs[] = {{out, rows * D * 2, "out"}, {lse, rows * 4, "lse"}, {s->workspace, (int64_t)need, "workspace"}};
+  const Range ins[] = {{q, qb, "q"}, {cu, (R + 1) * 4, "cu_seqlens"}, {kv_len, R * 4, "kv_len"},
+                       {table, R * s->max_blocks * 4, "block_table"},
+                       {k_pool, slabs * s->block_size * D, "k_pool"}, {v_pool, slabs * s->block_size * D, "v_pool"},
+                       {k_scale, slabs * 4, "k_scale"}, {v_scale, slabs * 4, "v_scale"}};
+  if (need) {
+    if (!s->workspace || s->workspace_bytes < need)
+      return fail(HELM_E_WORKSPACE, "workspace of %zu bytes at %p; %zu bytes needed", s->workspace_bytes,
+                  s->workspace, need);
+    if ((uintptr_t)s->workspace % kAlign)
+      return fail(HELM_E_WORKSPACE, "workspace %p is not %zu-byte aligned", s->workspace, kAlign);
+  }
+  if ((rc = check_alias(outs, need ? 3 : 2, ins, 8)) != HELM_OK) return rc;
+  rc = device_gate(-1);
+  if (rc != HELM_OK) return rc;
+  a.c = cache_of(s, k_pool, v_pool, k_scale, v_scale, table);
+  a.q = (const uint16_t*)q; a.cu = cu; a.kv_len = kv_len;
+  a.out = (uint16_t*)out; a.lse = lse; a.part = (float*)s->workspace;
+  return launch_status(helm::launch_kv8_attend(a, (hipStream_t)s->stream), "8-bit cache attention launch");
+}
+
+int helm_kv8_weigh(const void* q, const float* lse, const int32_t* cu, const int32_t* kv_len, const int32_t* table,
+                   const void* k_pool, const float* k_scale, float* weights, const helm_kv8_shape_t* s) {
+  clear_error();
+  int rc = check_kv8(s);
+  if (rc != HELM_OK || (rc = check_queries(s)) != HELM_OK) return rc;
+  if (s->n_tokens == 0 || s->max_kv_len == 0) return HELM_OK;
+  if (!q || !lse || !cu || !kv_len || !table || !k_pool || !k_scale || !weights)
+    return fail(HELM_E_INVALID_ARG, "a tensor pointer is NULL");
+  const int64_t D = s->head_dim, R = s->n_requests, slabs = (int64_t)s->n_blocks * s->n_kv_heads;
+  const int64_t qb = span_bytes(s->n_tokens, s->n_q_heads, D, s->tok_stride, s->head_stride, 2);
+  if (qb < 0) return fail(HELM_E_INVALID_ARG, "strides of q are not positive or overflow");
+  if ((rc = check_aligned(q, "q", 2)) || (rc = check_aligned(k_pool, "k_pool", 16))) return rc;
+  const Range outs[] = {{weights, slabs * s->block_size * 4, "weights"}};
+  const Range ins[] = {{q, qb, "q"}, {lse, s->n_tokens * s->n_q_heads * 4, "lse"}, {cu, (R + 1) * 4, "cu_seqlens"},
+                       {kv_len, R * 4, "kv_len"}, {table, R * s->max_blocks * 4, "block_table"},
+                       {k_pool, slabs * s->block_size * D, "k_pool"}, {k_scale, slabs * 4, "k_scale"}};
+  if ((rc = check_alias(outs, 1, ins, 7)) != HELM_OK) return rc;
+  rc = device_gate(-1);
+  if (rc != HELM_OK) return rc;
+  helm::Kv8AttendArgs a = attend_args(s);
+  const int32_t longest = a.c.max_len;
+  a.c = cache_of(s, k_pool, nullptr, k_scale, nullptr, table);
+  a.c.max_len = longest;
+  a.q = (const uint16_t*)q; a.cu = cu; a.kv_len = kv_len;
+  a.lse = const_cast<float*>(lse); a.weights = weights;
+  return launch_status(helm::launch_kv8_weigh(a, (hipStream_t)s->stream), "accumulated weight launch");
+}
+
+static int check_evict(const helm_kv8_evict_shape_t* s) {
+  if (!s) return fail(HELM_E_INVALID_ARG, "shape is NULL");
+  int rc = check_cache(s->n_kv_heads, s->head_dim, s->block_size, s->n_blocks, s->n_requests, s->max_kv_len);
+  if (rc != HELM_OK) return rc;
+  if (s->max_blocks_src < 1 || s->max_blocks_dst < 1)
+    return fail(HELM_E_INVALID_ARG, "max_blocks_src=%d and max_blocks_dst=%d must be >= 1", s->max_blocks_src,
+                s->max_blocks_dst);
+  if (s->budget < 1 || s->budget > (int64_t)s->max_blocks_dst * s->block_size)
+    return fail(HELM_E_INVALID_ARG, "budget=%d must lie in 1..max_blocks_dst * block_size (%lld)", s->budget,
+                (long long)s->max_blocks_dst * s->block_size);
+  if (s->recent < 0 || s->recent > s->budget)
+    return fail(HELM_E_INVALID_ARG, "recent=%d must lie in 0..budget (%d)", s->recent, s->budget);
+  int64_t n = s->n_requests;
+  if (!mul_ok(n, s->n_kv_heads) || !mul_ok(n, (int64_t)s->budget * 4))
+    return fail(HELM_E_INVALID_ARG, "kept overflows int64");
+  return HELM_OK;
+}
+
+int helm_kv8_evict(const int32_t* kv_len, const int32_t* src, const int32_t* dst, void* k_pool, void* v_pool,
+                   float* k_scale, float* v_scale, float* weights, int32_t* kept, int32_t* new_len,
+                   const helm_kv8_evict_shape_t* s) {
+  clear_error();
+  int rc = check_evict(s);
+  if (rc != HELM_OK) return rc;
+  if (!kv_len || !src || !dst || !k_pool || !v_pool || !k_scale || !v_scale || !weights || !kept || !new_len)
+    return fail(HELM_E_INVALID_ARG, "a tensor pointer is NULL");
+  if ((rc = check_aligned(k_pool, "k_pool", 16)) || (rc = check_aligned(v_pool, "v_pool", 16))) return rc;
+  const int64_t R = s->n_requests, slabs = (int64_t)s->n_blocks * s->n_kv_heads;
+  const int64_t pool = slabs * s->block_size * s->head_dim;
+  const Range outs[] = {{k_pool, pool, "k_pool"}, {v_pool, pool, "v_pool"}, {k_scale, slabs * 4, "k_scale"},
+                        {v_scale, slabs * 4, "v_scale"}, {weights, slabs * s->block_size * 4, "weights"},
+                        {kept, R * s->n_kv_heads * s->budget * 4, "kept"}, {new_len, R * 4, "new_len"}};
+  const Range ins[] = {{kv_len, R * 4, "kv_len"}, {src, R * s->max_blocks_src * 4, "src_block_table"},
+                       {dst, R * s->max_blocks_dst * 4, "dst_block_table"}};
+  if ((rc = check_alias(outs, 7, ins, 3)) != HELM_OK) return rc;
+  rc = device_gate(-1);
+  if (rc != HELM_OK) return rc;
+  helm::Kv8EvictArgs a{};
+  a.c.k_pool = (uint8_t*)k_pool; a.c.v_pool = (uint8_t*)v_pool; a.c.k_scale = k_scale; a.c.v_scale = v_scale;
+  a.c.table = src;
+  a.c.H = s->n_kv_heads; a.c.D = s->head_dim; a.c.B = s->block_size; a.c.n_blocks = s->n_blocks;
+  a.c.R = s->n_requests; a.c.max_blocks = s->max_blocks_src;
+  a.c.max_len = (int32_t)s->max_kv_len;
+  a.c.page_magic = helm::page_magic_of(s->block_size);
+  a.dst = dst; a.max_dst = s->max_blocks_dst; a.kv_len = kv_len; a.weights = weights;
+  a.kept = kept; a.new_len = new_len; a.budget = s->budget; a.recent = s->recent;
+  return launch_status(helm::launch_kv8_evict(a, (hipStream_t)s->stream), "eviction launch");
+}
+
+// Marks the pages [0, ceil(len / B)) of one request's table row as used.
+static int use_pages(const int32_t* row, int32_t max_blocks, int64_t len, int32_t B, int32_t n_blocks, int r,
+                     const char* name, std::vector<char>& used) {
+  const int64_t pages = (len + B - 1) / B;
+  if (pages > max_blocks)
+    return fail(HELM_E_PAGED_TABLE, "request %d needs %lld pages; %s has %d a row", r, (long long)pages, name,
+                max_blocks);
+  for (int64_t p = 0; p < pages; ++p) {
+    if (row[p] < 0 || row[p] >= n_blocks)
+      return fail(HELM_E_PAGED_TABLE, "%s[%d][%lld] = %d lies outside [0, %d)", name, r, (long long)p, row[p],
+                  n_blocks);
+    if (used[(size_t)row[p]])
+      return fail(HELM_E_PAGED_TABLE, "block %d is used twice (%s, request %d, page %lld)", row[p], name, r,
+                  (long long)p);
+    used[(size_t)row[p]] = 1;
+  }
+  return HELM_OK;
+}
+
+int helm_kv8_check(const helm_kv8_shape_t* s, const int32_t* cu, const int32_t* kv_len, const int32_t* table) {
+  clear_error();
+  int rc = check_kv8(s);
+  if (rc != HELM_OK) return rc;
+  if (!cu || !kv_len || !table) return fail(HELM_E_INVALID_ARG, "a host pointer is NULL");
+  if (cu[0] != 0) return fail(HELM_E_PAGED_TABLE, "cu_seqlens[0] = %d", cu[0]);
+  if (cu[s->n_requests] != s->n_tokens)
+    return fail(HELM_E_PAGED_TABLE, "cu_seqlens[R] = %d but n_tokens = %lld", cu[s->n_requests],
+                (long long)s->n_tokens);
+  try {
+    std::vector<char> used((size_t)s->n_blocks, 0);
+    for (int r = 0; r < s->n_requests; ++r) {
+      if (cu[r + 1] < cu[r]) return fail(HELM_E_PAGED_TABLE, "cu_seqlens decreases at request %d", r);
+      if (kv_len[r] < cu[r + 1] - cu[r])
+        return fail(HELM_E_PAGED_TABLE, "kv_len[%d] = %d is less than its %d queries", r, kv_len[r],
+                    cu[r + 1] - cu[r]);
+      if (kv_len[r] > s->max_kv_len)
+        return fail(HELM_E_PAGED_TABLE, "kv_len[%d] = %d exceeds max_kv_len", r, kv_len[r]);
+      rc = use_pages(table + (int64_t)r * s->max_blocks, s->max_blocks, kv_len[r], s->block_size, s->n_blocks, r,
+                     "block_table", used);
+      if (rc != HELM_OK) return rc;
+    }
+  } catch (const std::bad_alloc&) {
+    return fail(HELM_E_INVALID_ARG, "no host memory for %d blocks", s->n_blocks);
+  }
+  return HELM_OK;
+}
+
+int helm_kv8_evict_check(const helm_kv8_evict_shape_t* s, const int32_t* kv_len, const int32_t* src,
+                         const int32_t* dst) {
+  clear_error();
+  int rc = check_evict(s);
+  if (rc != HELM_OK) return rc;
+  if (!kv_len || !src || !dst) return fail(HELM_E_INVALID_ARG, "a host pointer is NULL");
+  try {
+    std::vector<char> used((size_t)s->n_blocks, 0);
+    for (int r = 0; r < s->n_requests; ++r) {
+      if (kv_len[r] < 0 || kv_len[r] > s->max_kv_len)
+        return fail(HELM_E_PAGED_TABLE, "kv_len[%d] = %d lies outside 0..max_kv_len", r, kv_len[r]);
+      const int64_t keep = kv_len[r] < s->budget ? kv_len[r] : s->budget;
+      rc = use_pages(src + (int64_t)r * s->max_blocks_src, s->max_blocks_src, kv_len[r], s->block_size, s->n_blocks,
+                     r, "src_block_table", used);
+      if (rc != HELM_OK) return rc;
+      rc = use_pages(dst + (int64_t)r * s->max_blocks_dst, s->max_blocks_dst, keep, s->block_size, s->n_blocks, r,
+                     "dst_block_table", used);
+      if (rc != HELM_OK) return rc;
+    }
+  } catch (const std::bad_alloc&) {
+    return fail(HELM_E_INVALID_ARG, "no host memory for %d blocks", s->n_blocks);
+  }
+  return HELM_OK;
+}
+
+}  // extern "C"

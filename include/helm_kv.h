@@ -429,6 +429,197 @@ const char* helm_status_string(int status);
  * failing later). */
 int helm_abi_version(void);
 
+/* ==== Serving over a transferred cache ==================================
+ *
+ * What a server does with the target model's cache once a transfer has
+ * written it: rotate the next tokens' queries and keys, hold the cache in 8
+ * bits, attend over it, accumulate the weight each cached token receives and
+ * evict the tokens that receive the least.
+ *
+ * These calls share the conventions above (device pointers of the caller,
+ * asynchronous on the stream given, host validation before anything is
+ * enqueued, nothing allocated, device-side tables bounds-checked by the
+ * kernels).  They are safe to capture into a HIP graph: kernels only. */
+
+/* Rotary positions.  A head of head_dim values x is turned in its first
+ * rot_dim ones, P = rot_dim/2 pairs (a, b): (x[i], x[i+P]) in the HALF layout,
+ * (x[2i], x[2i+1]) in the INTERLEAVED one; the rest passes through:
+ *   (a, b) -> m (a cos - b sin, a sin + b cos),  angle = position * freq[i]
+ * with freq[i] from w_i = theta^(-2i/rot_dim) by the scaling (f = factor,
+ * L = original_len, the length the model was trained for):
+ *   PLAIN    w_i
+ *   LINEAR   w_i / f
+ *   NTK      w_i with theta * f^(rot_dim/(rot_dim-2)) as the base
+ *   YARN     w_i (r_i/f + 1 - r_i), r_i = clamp((i - lo)/(hi - lo), 0, 1),
+ *            lo = max(0, floor c(beta_fast)), hi = min(rot_dim-1, ceil c(beta_slow)),
+ *            c(n) = rot_dim ln(L/(2 pi n)) / (2 ln theta); hi - lo at least 0.001
+ *   BANDED   w_i ((1-k_i)/f + k_i), k_i = clamp((t_i - low_freq)/(high_freq - low_freq), 0, 1),
+ *            t_i = L w_i / (2 pi), the turns made over the original length
+ * and m = magnitude (0 selects 0.1 ln f + 1 for YARN, 1 otherwise).
+ * Modes: FORWARD; INVERSE undoes it (angle negated, 1/m), which takes a
+ * cached key back to content space; ADJOINT is the transpose (angle negated,
+ * m), the gradient of FORWARD.  Angles are formed in fp64 (reduced to a
+ * fraction of a turn before cos and sin are taken in fp32), the turn itself
+ * is fp32, and the result is rounded once to the storage type. */
+#define HELM_ROPE_MAX_PAIRS 128
+typedef enum { HELM_ROPE_HALF = 0, HELM_ROPE_INTERLEAVED = 1 } helm_rope_layout_t;
+typedef enum {
+  HELM_ROPE_PLAIN = 0, HELM_ROPE_LINEAR = 1, HELM_ROPE_NTK = 2, HELM_ROPE_YARN = 3, HELM_ROPE_BANDED = 4
+} helm_rope_scaling_t;
+typedef enum { HELM_ROPE_FORWARD = 0, HELM_ROPE_INVERSE = 1, HELM_ROPE_ADJOINT = 2 } helm_rope_mode_t;
+
+typedef struct {
+  int32_t head_dim;        /* 2..256 */
+  int32_t rot_dim;         /* even, 2..head_dim */
+  int32_t layout;          /* helm_rope_layout_t */
+  int32_t scaling;         /* helm_rope_scaling_t */
+  double theta;            /* > 0, finite; > 1 for YARN */
+  double factor;           /* > 0; PLAIN ignores it */
+  double original_len;     /* > 0 for YARN and BANDED */
+  double beta_fast, beta_slow;   /* YARN: > 0 (32 and 1 are usual) */
+  double low_freq, high_freq;    /* BANDED: low_freq < high_freq (1 and 4 are usual) */
+  double magnitude;        /* 0 = the scaling's own; helm_rope_plan writes the one in force */
+  int32_t planned;         /* set by helm_rope_plan */
+  int32_t reserved;
+  double freq[HELM_ROPE_MAX_PAIRS];   /* radians per position, written by helm_rope_plan */
+} helm_rope_t;
+
+/* Checks the description and fills in freq, magnitude and planned (host
+ * arithmetic only, no device). */
+int helm_rope_plan(helm_rope_t* rope);
+
+typedef struct {
+  int32_t n_q_heads;       /* >= 0; 0: q and out_q are not touched */
+  int32_t n_k_heads;       /* >= 0; 0: k and out_k are not touched */
+  int32_t dtype;           /* helm_dtype_t of q, k and the outputs */
+  int32_t mode;            /* helm_rope_mode_t */
+  int64_t n_tokens;        /* >= 0 */
+  /* element strides of a token and of a head (positive); a head's values are contiguous */
+  int64_t q_tok, q_head, k_tok, k_head, out_q_tok, out_q_head, out_k_tok, out_k_head;
+  void* stream;
+} helm_rope_shape_t;
+
+/* out_q, out_k = the turned q [n_tokens, n_q_heads, head_dim] and k
+ * [n_tokens, n_k_heads, head_dim] at pos [n_tokens] int32 (any values).  An
+ * output may be its own input (same address and strides), slices of one fused
+ * tensor included; any other overlap is refused with HELM_E_ALIAS. */
+int helm_rope(const void* q, const void* k, const int32_t* pos, void* out_q, void* out_k,
+              const helm_rope_t* rope, const helm_rope_shape_t* shape);
+
+/* The 8-bit paged cache of one layer.
+ *   k_pool, v_pool   : [n_blocks, H, block_size, D] e4m3 codes (OCP, no infinity)
+ *   k_scale, v_scale : [n_blocks, H] fp32; a code stands for code * scale
+ *   weights          : [n_blocks, H, block_size] fp32, accumulated weights
+ *   block_table      : [R, max_blocks] int32; token t of request r is in slot
+ *                      t % block_size of block block_table[r][t / block_size]
+ * A block's tokens of one head are contiguous: the unit that has one scale is
+ * also the unit that attention streams.  helm_kv8_store and helm_kv8_evict
+ * write scales that are powers of two 2^e, the smallest e in -120..120 with
+ * max|x| <= 448 * 2^e: e4m3 keeps its relative precision at any scale, and a
+ * code taken to another such scale changes its exponent only (bits are lost
+ * only below e4m3's smallest normal value).  helm_kv8_attend and
+ * helm_kv8_weigh take any finite positive scale.
+ * A table entry outside [0, n_blocks) makes its tokens absent: they are not
+ * stored, and attention masks them. */
+typedef struct {
+  int32_t n_q_heads;       /* a multiple of n_kv_heads (attend, weigh) */
+  int32_t n_kv_heads;      /* H >= 1 */
+  int32_t head_dim;        /* D in {64, 128} */
+  int32_t dtype;           /* of k, v in helm_kv8_store; q and out are HELM_BF16 */
+  int32_t block_size;      /* a multiple of 16, 16..256 */
+  int32_t n_blocks;        /* >= 1 */
+  int32_t n_requests;      /* R >= 1 */
+  int32_t max_blocks;      /* row stride of block_table, >= 1 */
+  int32_t causal;          /* 1: query i of n of a request with kv_len tokens sees
+                              tokens 0 .. kv_len - n + i; 0: all of them */
+  int32_t window;          /* > 0: only the last `window` of those (causal only); 0: no limit */
+  int64_t n_tokens;        /* tokens in q, or in k and v: cu_seqlens[R] */
+  int64_t max_kv_len;      /* bound on kv_len (kv_start + new tokens) over the requests;
+                              tokens past it, or past max_blocks * block_size, are absent */
+  int64_t tok_stride, head_stride;       /* elements; of q (attend, weigh) or k (store) */
+  int64_t v_tok_stride, v_head_stride;   /* of v (store) */
+  double softmax_scale;    /* finite */
+  void* stream;
+  void* workspace;         /* helm_kv8_attend */
+  size_t workspace_bytes;
+} helm_kv8_shape_t;
+
+/* Stores new tokens in 8 bits: token i of request r (packed index
+ * cu_seqlens[r] + i of k, v [n_tokens, H, D]) becomes the request's token
+ * kv_start[r] + i.
+ * A block that held tokens of its request before (kv_start inside it) keeps
+ * the larger of its scale and the one the new tokens need; where that grows
+ * it, the tokens held are re-coded.  Codes round to nearest even; infinities
+ * saturate to +-448 and do not count in max|x|; NaN stays NaN.
+ *   cu_seqlens : [R+1] int32;  kv_start : [R] int32, >= 0
+ *   weights    : NULL, or the accumulated weights, set to 0 for stored tokens
+ * Blocks belong to one request each. */
+int helm_kv8_store(const void* k, const void* v, const int32_t* cu_seqlens, const int32_t* kv_start,
+                   const int32_t* block_table, void* k_pool, void* v_pool, float* k_scale, float* v_scale,
+                   float* weights, const helm_kv8_shape_t* shape);
+
+/* Attention of packed queries over the 8-bit cache, for single tokens
+ * (decode) and for whole prompts:
+ *   s_j = softmax_scale * q . (k_code_j * k_scale),  p = softmax over the tokens seen
+ *   out = sum_j p_j (v_code_j * v_scale),  lse = ln sum_j exp(s_j)
+ *   q, out : [n_tokens, n_q_heads, D] bf16 (out contiguous);  lse : [n_tokens, n_q_heads] fp32
+ *   kv_len : [R] int32, tokens in the cache, the queries' own included
+ * Query head g attends KV head g / (n_q_heads / n_kv_heads).  A query that
+ * sees nothing gives out = 0, lse = -inf.  Products are exact bf16 ones with
+ * fp32 accumulation, statistics fp32; p is rounded to bf16 as the operand of
+ * its product with V.  A NaN code inside a request's length spoils the
+ * queries of its tile; codes past the length are never used.  The workspace
+ * (helm_kv8_attend_workspace_bytes, 256-byte aligned) holds the partial
+ * results of a long context's pieces. */
+size_t helm_kv8_attend_workspace_bytes(const helm_kv8_shape_t* shape);
+int helm_kv8_attend(const void* q, const int32_t* cu_seqlens, const int32_t* kv_len, const int32_t* block_table,
+                    const void* k_pool, const void* v_pool, const float* k_scale, const float* v_scale,
+                    void* out, float* lse, const helm_kv8_shape_t* shape);
+
+/* Adds to weights the softmax weight that each cached token receives from
+ * these queries, summed over the queries and the query heads of its KV head:
+ *   weights[block, h, slot] += sum exp(s_j - lse)
+ * with lse as helm_kv8_attend returned it (a query whose lse is not finite
+ * adds nothing).  Each weight has one owner: the order of its sum is fixed. */
+int helm_kv8_weigh(const void* q, const float* lse, const int32_t* cu_seqlens, const int32_t* kv_len,
+                   const int32_t* block_table, const void* k_pool, const float* k_scale, float* weights,
+                   const helm_kv8_shape_t* shape);
+
+/* Eviction by accumulated weight.  Of each request's kv_len tokens, per KV
+ * head, min(kv_len, budget) stay: the `recent` last ones and those with the
+ * largest weights, ties to the lowest index, NaN below every number.  They
+ * are copied, in order, into the blocks of dst_table (positions stay folded
+ * into the keys); every block so written is written whole (zeros past the
+ * last token) and gets its own scale, and the kept weights go with their
+ * tokens.
+ *   src_block_table [R, max_blocks_src], dst_block_table [R, max_blocks_dst] int32,
+ *     both into the same pools; no block is in both, or twice in dst
+ *   kept    : [R, H, budget] int32, the kept tokens' old indices, ascending, -1 beyond
+ *   new_len : [R] int32
+ * Workspace: none. */
+typedef struct {
+  int32_t n_kv_heads, head_dim, block_size, n_blocks, n_requests;   /* as in helm_kv8_shape_t */
+  int32_t max_blocks_src, max_blocks_dst;   /* row strides; max_blocks_dst * block_size >= budget */
+  int32_t budget;          /* >= 1 */
+  int32_t recent;          /* 0..budget */
+  int32_t reserved;
+  int64_t max_kv_len;      /* bound on kv_len; longer ones are cut to it */
+  void* stream;
+} helm_kv8_evict_shape_t;
+
+int helm_kv8_evict(const int32_t* kv_len, const int32_t* src_block_table, const int32_t* dst_block_table,
+                   void* k_pool, void* v_pool, float* k_scale, float* v_scale, float* weights,
+                   int32_t* kept, int32_t* new_len, const helm_kv8_evict_shape_t* shape);
+
+/* Checks host copies of the tables that a call would use: cu_seqlens (0
+ * first, non-decreasing, n_tokens last), lengths (kv_len >= the request's
+ * queries), and that every page in use is a block of the pool and no block is
+ * used twice.  HELM_E_PAGED_TABLE otherwise. */
+int helm_kv8_check(const helm_kv8_shape_t* shape, const int32_t* cu_seqlens_host, const int32_t* kv_len_host,
+                   const int32_t* block_table_host);
+int helm_kv8_evict_check(const helm_kv8_evict_shape_t* shape, const int32_t* kv_len_host,
+                         const int32_t* src_block_table_host, const int32_t* dst_block_table_host);
+
 #ifdef __cplusplus
 }  /* extern "C" */
 #endif
