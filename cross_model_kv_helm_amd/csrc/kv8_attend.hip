@@ -3,7 +3,9 @@
 //
 // Matrix products are v_mfma_f32_16x16x32_bf16 with both codes taken to bf16
 // (exact: e4m3 has fewer bits) and q as it is; a block's scale multiplies the
-// scores of its tokens (K) and their probabilities (V) instead of the codes.
+// scores of its tokens (K) and, as log2 added to the exponent, their
+// probabilities (V) instead of the codes: a token far below the maximum whose
+// values are large does not underflow on the way.
 // Scores are formed transposed, S^T = K Q^T: in the result a lane holds four
 // tokens of one query row, which is where the second product, O^T = V^T P^T,
 // takes its right operand from — P never leaves the registers.  The order of
@@ -192,6 +194,7 @@ __global__ void __launch_bounds__(kThreads) kv8_attend_kernel(Kv8AttendArgs a) {
     u32x4 kw[2][D / 64];
     uint32_t vw[2][4][D / 64];
     float ks[2], vs[2];
+    bool odd = t0 + kStep > q.len;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       x[u] = tile_at(c, table, h, t0 + 16 * u, q.len);
@@ -209,19 +212,27 @@ __global__ void __launch_bounds__(kThreads) kv8_attend_kernel(Kv8AttendArgs a) {
       }
       ks[u] = c.k_scale[x[u].slab] * a.scale_log2;
       vs[u] = c.v_scale[x[u].slab];
+      odd |= !x[u].ok || !(vs[u] > 0.0f);
     }
     // tokens past the context are not read as numbers: their codes may be anything
-    if (t0 + kStep > q.len || !x[0].ok || !x[1].ok) {
+    if (odd) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        if (!x[u].ok) vs[u] = 0.0f;
+        const bool none = !x[u].ok || !(vs[u] > 0.0f);
+        if (none) vs[u] = 1.0f;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (!x[u].ok || t0 + 16 * u + 4 * g + i >= q.len) {
+          if (none || t0 + 16 * u + 4 * g + i >= q.len) {
 #pragma unroll
             for (int b = 0; b < D / 64; ++b) vw[u][i][b] = 0u;
           }
       }
+    }
+    float lv[2], inv[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      lv[u] = __builtin_amdgcn_logf(vs[u]);
+      inv[u] = __builtin_amdgcn_rcpf(vs[u]);
     }
     const bool all_seen = t0 >= s_last.lo && t0 + kStep <= s_first.hi && x[0].ok && x[1].ok;
 
@@ -233,7 +244,7 @@ __global__ void __launch_bounds__(kThreads) kv8_attend_kernel(Kv8AttendArgs a) {
       for (int u = 0; u < 2; ++u) {
         const f32x4 s = scores<D>(kw[u], qv[t]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[4 * u + i] = s[i] * ks[u];
+        for (int i = 0; i < 4; ++i) y[4 * u + i] = fmaf(s[i], ks[u], lv[u]);
       }
       if (!all_seen) {
 #pragma unroll
@@ -244,9 +255,9 @@ __global__ void __launch_bounds__(kThreads) kv8_attend_kernel(Kv8AttendArgs a) {
             if (!x[u].ok || tok < see[t].lo || tok >= see[t].hi) y[4 * u + i] = -INFINITY;
           }
       }
-      float top = y[0];
-#pragma unroll
-      for (int i = 1; i < 8; ++i) top = fmaxf(top, y[i]);
+      const float top0 = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) - lv[0];
+      const float top1 = fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])) - lv[1];
+      float top = fmaxf(top0, top1);
       if (__any(top > mref[t] + kLazy)) {
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
@@ -259,9 +270,9 @@ __global__ void __launch_bounds__(kThreads) kv8_attend_kernel(Kv8AttendArgs a) {
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float p = __builtin_amdgcn_exp2f(y[i] - mref[t]);
-        l[t] += p;
-        pv[t][i] = (__bf16)(p * vs[i >> 2]);
+        const float p = __builtin_amdgcn_exp2f(y[i] - mref[t]);   // probability times the value's scale
+        l[t] = fmaf(p, inv[i >> 2], l[t]);
+        pv[t][i] = (__bf16)p;
       }
     }
 #pragma unroll
@@ -327,32 +338,49 @@ __global__ void __launch_bounds__(kThreads) kv8_attend_kernel(Kv8AttendArgs a) {
   }
 }
 
-// Joins the pieces of a split context: one wave per (query, head).
+// Joins the pieces of a split context: one workgroup per (query, head), its
+// threads side by side over the D values and, in kThreads * 4 / D groups, over
+// the pieces.
 template <int D>
 __global__ void __launch_bounds__(kThreads) kv8_join_kernel(Kv8AttendArgs a) {
-  const int64_t rows = a.n_tok * a.Hq;
-  const int64_t at = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
-  if (at >= rows) return;
-  const int lane = threadIdx.x & 63;
+  constexpr int NG = kThreads * 4 / D;
+  __shared__ float red_m[kWaves], red_l[NG];
+  __shared__ f32x4 red_o[NG][D / 4];
+  const int64_t rows = a.n_tok * a.Hq, at = blockIdx.x;
+  const f32x2* ml = (const f32x2*)a.part + at;
   const float* part = a.part + 2 * (int64_t)a.splits * rows;
   float top = -3.402823466e38f;
-  for (int s = 0; s < a.splits; ++s) top = fmaxf(top, a.part[((int64_t)s * rows + at) * 2]);
-  float sum = 0.0f, v[D / 64] = {};
-  for (int s = 0; s < a.splits; ++s) {
-    const f32x2 ml = *(const f32x2*)(a.part + ((int64_t)s * rows + at) * 2);
-    if (ml[1] == 0.0f) continue;      // nothing seen there: no sums were written
-    const float f = exp2f(ml[0] - top);
-    sum += f * ml[1];
+  for (int s = threadIdx.x; s < a.splits; s += kThreads) top = fmaxf(top, ml[s * rows][0]);
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) v[i] += f * part[((int64_t)s * rows + at) * D + lane * (D / 64) + i];
+  for (int o = 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+  if ((threadIdx.x & 63) == 0) red_m[threadIdx.x >> 6] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) top = fmaxf(top, red_m[w]);
+  const int d = threadIdx.x % (D / 4), grp = threadIdx.x / (D / 4);
+  float sum = 0.0f;
+  f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int s = grp; s < a.splits; s += NG) {
+    const f32x2 x = ml[s * rows];
+    if (x[1] == 0.0f) continue;      // nothing seen there: no sums were written
+    const float f = exp2f(x[0] - top);
+    sum += f * x[1];
+    v += f * *(const f32x4*)(part + (s * rows + at) * D + 4 * d);
+  }
+  red_o[grp][d] = v;
+  if (d == 0) red_l[grp] = sum;
+  __syncthreads();
+  if (grp != 0) return;
+#pragma unroll
+  for (int i = 1; i < NG; ++i) {
+    sum += red_l[i];
+    v += red_o[i][d];
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-  for (int i = 0; i < D / 64; ++i) {
-    const __bf16 y = (__bf16)(v[i] * inv);
-    a.out[at * D + lane * (D / 64) + i] = __builtin_bit_cast(uint16_t, y);
-  }
-  if (lane == 0) a.lse[at] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+  const bf16x2 lo = {(__bf16)(v[0] * inv), (__bf16)(v[1] * inv)}, hi = {(__bf16)(v[2] * inv), (__bf16)(v[3] * inv)};
+  *(u32x2*)(a.out + at * D + 4 * d) = u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+  if (d == 0) a.lse[at] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 // ---- accumulated weight ---------------------------------------------------
@@ -445,7 +473,7 @@ hipError_t attend(const Kv8AttendArgs& a, hipStream_t stream) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   const int64_t rows = a.n_tok * a.Hq;
-  kv8_join_kernel<D><<<dim3((unsigned)((rows + kWaves - 1) / kWaves)), kThreads, 0, stream>>>(a);
+  kv8_join_kernel<D><<<dim3((unsigned)rows), kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 

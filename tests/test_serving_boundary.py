@@ -1,0 +1,260 @@
+"""The serving calls without a GPU: plans, workspace sizes, host checks of
+tables, and the refusals, all decided before any device work.  Calls with fake
+device pointers always carry a defect that host validation rejects first."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+
+import cross_model_kv_helm_amd as hk
+from tests import serving_ref as ref
+
+FAR = [ctypes.c_void_p((1 << 40) * (i + 1)) for i in range(12)]     # far apart: no overlaps
+
+
+def refused(rc, status, text):
+    assert rc == status, (rc, hk.helm_last_error())
+    assert text in hk.helm_last_error(), hk.helm_last_error()
+
+
+# ------------------------------------------------------------ rotary positions
+@pytest.mark.parametrize("scaling,name", list(enumerate(("plain", "linear", "ntk", "yarn", "banded"))))
+@pytest.mark.parametrize("rot,theta,factor,original", [(128, 1e6, 4.0, 32768.0), (2, 1e4, 2.0, 100.0),
+                                                       (34, 500.0, 1.5, 3000.0)])
+def test_rope_plan_frequencies(scaling, name, rot, theta, factor, original):
+    r = hk.make_rope(128, theta, rot_dim=rot, scaling=scaling, factor=factor, original_len=original)
+    want = ref.rope_frequencies(rot, theta, name, factor, original)
+    for a, b in zip(r.freq, want.tolist()):
+        assert abs(a - b) <= 1e-13 * b
+    assert not any(list(r.freq)[rot // 2:])
+    assert r.magnitude == (0.1 * math.log(factor) + 1.0 if name == "yarn" else 1.0)
+
+
+@pytest.mark.parametrize("kw,status,text", [
+    (dict(head_dim=1), 2, "head_dim"), (dict(head_dim=258), 2, "head_dim"), (dict(rot_dim=3), 2, "rot_dim"),
+    (dict(rot_dim=130), 2, "rot_dim"), (dict(rot_dim=0), 2, "rot_dim"), (dict(layout=2), 1, "layout"),
+    (dict(scaling=5), 1, "scaling"), (dict(theta=0.0), 1, "base"), (dict(theta=math.nan), 1, "base"),
+    (dict(scaling=1, factor=0.0), 1, "factor"), (dict(scaling=3, factor=2.0), 1, "original_len"),
+    (dict(scaling=3, factor=2.0, original_len=9.0, theta=1.0), 1, "base > 1"),
+    (dict(scaling=3, factor=2.0, original_len=9.0, beta_slow=0.0), 1, "beta"),
+    (dict(scaling=4, factor=2.0, original_len=9.0, low_freq=4.0), 1, "low_freq"),
+    (dict(magnitude=-1.0), 1, "magnitude"), (dict(magnitude=math.inf), 1, "magnitude"),
+    (dict(scaling=3, factor=1e-5, original_len=9.0), 1, "magnitude")])
+def test_rope_plan_refusals(kw, status, text):
+    args = dict(dict(head_dim=128, theta=1e6), **kw)
+    with pytest.raises(hk.HelmError) as e:
+        hk.make_rope(**args)
+    assert e.value.status == status and text in str(e.value)
+
+
+def rope_shape(**kw):
+    s = hk.HelmRopeShape(n_q_heads=2, n_k_heads=1, n_tokens=4, q_tok=256, q_head=128, k_tok=128, k_head=128,
+                         out_q_tok=256, out_q_head=128, out_k_tok=128, out_k_head=128)
+    for k, v in kw.items():
+        setattr(s, k, v)
+    return s
+
+
+def call_rope(s, ptrs=None, rope=None):
+    r = hk.make_rope(128, 1e6) if rope is None else rope
+    return hk.lib().helm_rope(*(FAR[:5] if ptrs is None else ptrs), ctypes.byref(r), ctypes.byref(s))
+
+
+def test_rope_refusals():
+    refused(call_rope(rope_shape(dtype=3)), 5, "dtype")
+    refused(call_rope(rope_shape(mode=3)), 1, "mode")
+    refused(call_rope(rope_shape(n_q_heads=-1)), 1, "head counts")
+    refused(call_rope(rope_shape(n_tokens=-1)), 1, "n_tokens")
+    refused(call_rope(rope_shape(q_tok=0)), 1, "strides")
+    refused(call_rope(rope_shape(out_k_head=-128)), 1, "strides")
+    refused(call_rope(rope_shape(q_tok=1 << 62)), 1, "strides")
+    refused(call_rope(rope_shape(), rope=hk.HelmRope(head_dim=128, rot_dim=128, theta=1e6)), 1, "helm_rope_plan")
+    assert call_rope(rope_shape(n_tokens=0)) == 0
+    assert call_rope(rope_shape(n_q_heads=0, n_k_heads=0)) == 0
+    for i, name in ((0, "q"), (1, "k"), (2, "pos"), (3, "out_q"), (4, "out_k")):
+        p = list(FAR[:5])
+        p[i] = None
+        refused(call_rope(rope_shape(), p), 1, "NULL")
+    p = list(FAR[:5])
+    p[1] = ctypes.c_void_p(p[1].value + 1)
+    refused(call_rope(rope_shape(), p), 1, "aligned")
+
+
+def test_rope_overlaps():
+    base = 1 << 40
+    q, k, pos, oq, ok = (ctypes.c_void_p(base * (i + 1)) for i in range(5))
+    refused(call_rope(rope_shape(), [q, k, pos, ctypes.c_void_p(q.value + 2), ok]), 8, "out_q overlaps q")
+    refused(call_rope(rope_shape(), [q, k, pos, oq, q]), 8, "out_k overlaps q")
+    refused(call_rope(rope_shape(), [q, k, pos, oq, oq]), 8, "out_k overlaps out_q")
+    refused(call_rope(rope_shape(), [q, k, pos, oq, pos]), 8, "overlaps pos")
+    refused(call_rope(rope_shape(out_q_tok=512), [q, k, pos, q, ok]), 8, "out_q overlaps q")   # other strides
+    # slices of one fused tensor [4, 3 heads, 128], in place: no refusal before the device gate
+    s = rope_shape(q_tok=384, k_tok=384, out_q_tok=384, out_k_tok=384)
+    kk = ctypes.c_void_p(q.value + 512)
+    if hk.helm_device_check(-1) == 4:
+        assert call_rope(s, [q, kk, pos, q, kk]) == 4
+    refused(call_rope(s, [q, kk, pos, q, ctypes.c_void_p(kk.value - 2)]), 8, "overlaps")
+
+
+# ------------------------------------------------------------ the 8-bit cache
+def shape(**kw):
+    s = hk.HelmKv8Shape(n_q_heads=16, n_kv_heads=8, head_dim=128, dtype=0, block_size=16, n_blocks=100, n_requests=2,
+                        max_blocks=8, causal=1, window=0, n_tokens=2, max_kv_len=128, tok_stride=2048, head_stride=128,
+                        v_tok_stride=1024, v_head_stride=128, softmax_scale=0.1)
+    for k, v in kw.items():
+        setattr(s, k, v)
+    return s
+
+
+def calls():
+    L = hk.lib()
+    return {"store": (L.helm_kv8_store, 10), "attend": (L.helm_kv8_attend, 10), "weigh": (L.helm_kv8_weigh, 8)}
+
+
+@pytest.mark.parametrize("name", ["store", "attend", "weigh"])
+@pytest.mark.parametrize("kw,status,text", [
+    (dict(n_kv_heads=0), 1, "n_kv_heads"), (dict(head_dim=96), 2, "head_dim"), (dict(block_size=8), 1, "block_size"),
+    (dict(block_size=24), 1, "block_size"), (dict(block_size=272), 1, "block_size"), (dict(n_blocks=0), 1, "n_blocks"),
+    (dict(n_requests=0), 1, "n_requests"), (dict(n_requests=32768), 1, "n_requests"),
+    (dict(max_blocks=0), 1, "max_blocks"), (dict(n_tokens=-1), 1, "n_tokens"), (dict(n_tokens=1 << 31), 1, "n_tokens"),
+    (dict(max_kv_len=-1), 1, "max_kv_len"), (dict(max_kv_len=(1 << 30) + 1), 1, "max_kv_len"),
+    (dict(tok_stride=0), 1, "strides"), (dict(tok_stride=1 << 62), 1, "strides")])
+def test_shapes_refused(name, kw, status, text):
+    f, n = calls()[name]
+    refused(f(*FAR[:n], ctypes.byref(shape(**kw))), status, text)
+    assert f(*FAR[:n], None) == 1
+
+
+@pytest.mark.parametrize("name", ["attend", "weigh"])
+@pytest.mark.parametrize("kw,status,text", [
+    (dict(n_q_heads=12), 1, "multiple"), (dict(n_q_heads=0), 1, "multiple"), (dict(dtype=1), 5, "bf16"),
+    (dict(causal=2), 1, "causal"), (dict(window=-1), 1, "window"), (dict(window=5, causal=0), 1, "window"),
+    (dict(softmax_scale=math.inf), 1, "softmax_scale"),
+    (dict(n_tokens=2 ** 31 - 1), 1, "n_tokens * n_q_heads")])
+def test_query_shapes_refused(name, kw, status, text):
+    f, n = calls()[name]
+    refused(f(*FAR[:n], ctypes.byref(shape(**kw))), status, text)
+
+
+def test_store_refusals():
+    f, n = calls()["store"]
+    refused(f(*FAR[:n], ctypes.byref(shape(dtype=2))), 5, "dtype")
+    refused(f(*FAR[:n], ctypes.byref(shape(v_tok_stride=-1))), 1, "strides")
+    assert f(*FAR[:n], ctypes.byref(shape(n_tokens=0))) == 0
+    for i in range(9):
+        p = list(FAR[:n])
+        p[i] = None
+        refused(f(*p, ctypes.byref(shape())), 1, "NULL")
+    for i, text in ((5, "k_pool is not"), (6, "v_pool is not")):
+        p = list(FAR[:n])
+        p[i] = ctypes.c_void_p(p[i].value + 8)
+        refused(f(*p, ctypes.byref(shape())), 1, text)
+    p = list(FAR[:n])
+    p[6] = p[5]
+    refused(f(*p, ctypes.byref(shape())), 8, "v_pool overlaps k_pool")
+    p = list(FAR[:n])
+    p[9] = p[0]
+    refused(f(*p, ctypes.byref(shape())), 8, "weights overlaps k")
+
+
+def test_attend_refusals_and_workspace():
+    f, n = calls()["attend"]
+    assert f(*FAR[:n], ctypes.byref(shape(n_tokens=0))) == 0
+    for i in range(n):
+        p = list(FAR[:n])
+        p[i] = None
+        refused(f(*p, ctypes.byref(shape())), 1, "NULL")
+    p = list(FAR[:n])
+    p[8] = p[5]
+    refused(f(*p, ctypes.byref(shape())), 8, "out overlaps v_pool")
+    p = list(FAR[:n])
+    p[8] = ctypes.c_void_p(p[8].value + 2)
+    refused(f(*p, ctypes.byref(shape())), 1, "out is not 16-byte aligned")
+    # a long context is split: its pieces need the workspace; the size is a multiple of 256
+    s = shape(max_blocks=8192, n_blocks=8192, max_kv_len=131072, n_requests=1, n_tokens=1)
+    need = hk.helm_kv8_attend_workspace_bytes(s)
+    assert need > 256 and need % 256 == 0
+    refused(f(*FAR[:n], ctypes.byref(s)), 7, "bytes needed")
+    s.workspace, s.workspace_bytes = FAR[11].value, need - 256
+    refused(f(*FAR[:n], ctypes.byref(s)), 7, "bytes needed")
+    s.workspace, s.workspace_bytes = FAR[11].value + 16, need + 256
+    refused(f(*FAR[:n], ctypes.byref(s)), 7, "aligned")
+    s.workspace = FAR[4].value
+    refused(f(*FAR[:n], ctypes.byref(s)), 8, "workspace overlaps k_pool")
+    assert hk.lib().helm_kv8_attend_workspace_bytes(ctypes.byref(shape(head_dim=32))) == 0
+    assert hk.lib().helm_kv8_attend_workspace_bytes(None) == 0
+
+
+def test_weigh_refusals():
+    f, n = calls()["weigh"]
+    assert f(*FAR[:n], ctypes.byref(shape(n_tokens=0))) == 0
+    for i in range(n):
+        p = list(FAR[:n])
+        p[i] = None
+        refused(f(*p, ctypes.byref(shape())), 1, "NULL")
+    p = list(FAR[:n])
+    p[7] = p[1]
+    refused(f(*p, ctypes.byref(shape())), 8, "weights overlaps lse")
+
+
+def evict_shape(**kw):
+    s = hk.HelmKv8EvictShape(n_kv_heads=2, head_dim=64, block_size=16, n_blocks=20, n_requests=2, max_blocks_src=4,
+                             max_blocks_dst=2, budget=20, recent=4, max_kv_len=64)
+    for k, v in kw.items():
+        setattr(s, k, v)
+    return s
+
+
+@pytest.mark.parametrize("kw,text", [
+    (dict(n_requests=32767, n_kv_heads=65535, block_size=256, max_blocks_dst=1 << 23, budget=(1 << 31) - 1), "kept"),
+    (dict(budget=0), "budget"), (dict(budget=33), "budget"), (dict(recent=21), "recent"), (dict(recent=-1), "recent"),
+    (dict(max_blocks_src=0), "max_blocks_src"), (dict(block_size=20), "block_size"), (dict(max_kv_len=-1), "max_kv_len")])
+def test_evict_refusals(kw, text):
+    refused(hk.lib().helm_kv8_evict(*FAR[:10], ctypes.byref(evict_shape(**kw))), 1, text)
+
+
+def test_evict_pointers():
+    f = hk.lib().helm_kv8_evict
+    for i in range(10):
+        p = list(FAR[:10])
+        p[i] = None
+        refused(f(*p, ctypes.byref(evict_shape())), 1, "NULL")
+    p = list(FAR[:10])
+    p[8] = p[0]
+    refused(f(*p, ctypes.byref(evict_shape())), 8, "kept overlaps kv_len")
+    assert f(*FAR[:10], None) == 1
+
+
+def test_host_checks_of_tables():
+    s = shape(n_tokens=3, n_blocks=6, max_blocks=3, max_kv_len=48)
+    cu, kv = np.array([0, 1, 3]), np.array([17, 40])
+    table = np.array([[5, 0, -1], [1, 2, 3]])
+    assert hk.helm_kv8_check(s, cu, kv, table) == 0, hk.helm_last_error()
+    refused(hk.helm_kv8_check(s, np.array([1, 1, 3]), kv, table), 9, "cu_seqlens[0]")
+    refused(hk.helm_kv8_check(s, np.array([0, 1, 2]), kv, table), 9, "n_tokens")
+    refused(hk.helm_kv8_check(s, np.array([0, 4, 3]), kv, table), 9, "decreases")
+    refused(hk.helm_kv8_check(s, cu, np.array([17, 1]), table), 9, "queries")
+    refused(hk.helm_kv8_check(s, cu, np.array([17, 49]), table), 9, "max_kv_len")
+    refused(hk.helm_kv8_check(shape(n_tokens=3, n_blocks=6, max_blocks=2, max_kv_len=48), cu, kv, table[:, :2]), 9,
+            "needs 3 pages")
+    bad = table.copy()
+    bad[1, 2] = 6
+    refused(hk.helm_kv8_check(s, cu, kv, bad), 9, "outside")
+    bad[1, 2] = 5
+    refused(hk.helm_kv8_check(s, cu, kv, bad), 9, "used twice")
+    e = evict_shape()
+    src, dst = np.array([[0, 1, 2, 3], [4, -1, -1, -1]]), np.array([[5, 6], [7, -1]])
+    assert hk.helm_kv8_evict_check(e, np.array([64, 10]), src, dst) == 0, hk.helm_last_error()
+    refused(hk.helm_kv8_evict_check(e, np.array([64, 17]), src, dst), 9, "src_block_table[1][1]")
+    refused(hk.helm_kv8_evict_check(e, np.array([64, 10]), src, np.array([[5, 2], [7, -1]])), 9, "used twice")
+    refused(hk.helm_kv8_evict_check(e, np.array([65, 10]), src, dst), 9, "max_kv_len")
+
+
+def test_binding_checks():
+    import torch
+    t = torch.zeros((2, 3, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="must live on the GPU"):
+        hk._heads_ptr(t, "q", torch.bfloat16, (2, 3, 64))
+    with pytest.raises(ValueError, match="q or k"):
+        hk.helm_rope(None, None, None, hk.make_rope(64, 1e6))

@@ -1,0 +1,463 @@
+"""Serving over a transferred cache on the GPU — helm_rope, helm_kv8_store,
+helm_kv8_attend, helm_kv8_weigh, helm_kv8_evict — against the plain fp64
+implementations of tests/serving_ref.py, at the sizes and masks where they can
+go wrong.  Codes, scales, kept indices and moved weights have to be equal;
+computed numbers lie within tolerances counted from the roundings."""
+import math
+
+import pytest
+import torch
+
+from tests import serving_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def hk():
+    import cross_model_kv_helm_amd as hk
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    assert hk.helm_device_check(-1) == 0, hk.helm_last_error()
+    return hk
+
+
+def say(*a):
+    print("[serving]", *a, flush=True)
+
+
+def gen_of(seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return g
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32)
+
+
+def same_bits(a, b):
+    return torch.equal(a.cpu().contiguous().view(torch.uint8), b.cpu().contiguous().view(torch.uint8))
+
+
+TINY = torch.finfo(torch.float32).tiny      # of bf16 too: a result below it has no normal number, 0 stands for it
+
+
+def within(got, want, tol, what):
+    got, want = got.double().cpu(), want.cpu()
+    got, want = (x.masked_fill(x.abs() < TINY, 0.0) for x in (got, want))
+    fine = torch.isfinite(want)
+    assert torch.equal(torch.isfinite(got), fine) and torch.equal(got[~fine], want[~fine]), what
+    off = (got - want).abs()[fine]
+    worst = float((off / tol.cpu()[fine].clamp(min=1e-300)).max()) if off.numel() else 0.0
+    say(what, "worst error / tolerance", round(worst, 4))
+    assert worst <= 1.0, (what, worst)
+
+
+# ------------------------------------------------------------ rotary positions
+def rope_plan(hk, D, rot, layout, scaling, theta=1e6, **kw):
+    return hk.make_rope(D, theta, rot_dim=rot, layout=getattr(hk, "HELM_ROPE_" + layout.upper()),
+                        scaling=getattr(hk, "HELM_ROPE_" + scaling.upper()), **kw)
+
+
+def check_rope(x, got, pos, freq, layout, m, mode, what):
+    want, size = ref.rope(x, pos, freq, layout, m, mode)
+    # angle: fp64 product and reduction (2^-52 of it), rounded to fp32 as part of a turn; cos, sin, the
+    # magnitude, two products and a sum in fp32: 10 half-steps of the values turned; one rounding at the end
+    far = 2.0 ** -52 * pos.double().abs()[:, None, None]
+    tol = (10 * 2.0 ** -24 + far) * size + ref.HALF[x.dtype] * want.abs() * (1 + 2.0 ** -8)
+    within(got, want, tol, what)
+
+
+@pytest.mark.parametrize("D,rot,Hq,H,N,layout,scaling,dtype", [
+    (128, 128, 5, 1, 7, "half", "plain", torch.bfloat16),
+    (128, 64, 8, 2, 33, "interleaved", "linear", torch.bfloat16),
+    (64, 64, 1, 1, 1, "half", "ntk", torch.float32),
+    (96, 34, 3, 3, 19, "half", "yarn", torch.bfloat16),        # 17 pairs: no 16-byte pieces
+    (96, 30, 2, 4, 130, "interleaved", "banded", torch.float32),
+    (256, 256, 2, 1, 5, "interleaved", "yarn", torch.float32),
+    (81, 2, 4, 1, 3, "half", "ntk", torch.bfloat16),           # one pair, odd head
+    (128, 128, 40, 8, 3000, "half", "yarn", torch.bfloat16)])
+def test_rope_forward_inverse_adjoint(hk, D, rot, Hq, H, N, layout, scaling, dtype):
+    g = gen_of(D + rot + N)
+    spec = dict(factor=4.0, original_len=4096.0)
+    plan = rope_plan(hk, D, rot, layout, scaling, **spec)
+    freq = ref.rope_frequencies(rot, 1e6, scaling, 4.0, 4096.0)
+    m = 0.1 * math.log(4.0) + 1.0 if scaling == "yarn" else 1.0
+    assert max(abs(a - float(b)) / float(b) for a, b in zip(plan.freq, freq)) < 1e-14
+    q, k = (torch.randn((N, h, D), generator=g).to(dtype) for h in (Hq, H))
+    pos = torch.randint(-100, 200000, (N,), generator=g).to(torch.int32)
+    for mode in ("forward", "inverse", "adjoint"):
+        oq, ok = hk.helm_rope(q.cuda(), k.cuda(), pos.cuda(), plan, getattr(hk, "HELM_ROPE_" + mode.upper()))
+        check_rope(q, oq, pos, freq, layout, m, mode, f"rope {mode} q")
+        check_rope(k, ok, pos, freq, layout, m, mode, f"rope {mode} k")
+
+
+def test_rope_far_positions_and_one_operand(hk):
+    plan = rope_plan(hk, 128, 128, "half", "plain", theta=1e4)
+    freq = ref.rope_frequencies(128, 1e4)
+    k = torch.randn((4, 2, 128), generator=gen_of(1))
+    pos = i32([2 ** 31 - 1, -2 ** 31, 2 ** 24 + 1, 0])
+    q, ok = hk.helm_rope(None, k.cuda(), pos.cuda(), plan)
+    assert q is None
+    check_rope(k, ok, pos, freq, "half", 1.0, "forward", "rope far")
+    oq, none = hk.helm_rope(k.cuda(), None, pos.cuda(), plan)
+    assert none is None and same_bits(oq, ok)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rope_in_place_on_slices_of_a_fused_tensor(hk, dtype):
+    Hq, H, D, N = 6, 2, 64, 37
+    x = torch.randn((N, Hq + 2 * H, D), generator=gen_of(2)).to(dtype)
+    plan = rope_plan(hk, D, 32, "interleaved", "plain")
+    freq = ref.rope_frequencies(32, 1e6)
+    pos = torch.arange(N, dtype=torch.int32) * 977
+    y = x.cuda()
+    hk.helm_rope(y[:, :Hq], y[:, Hq:Hq + H], pos.cuda(), plan, out_q=y[:, :Hq], out_k=y[:, Hq:Hq + H])
+    check_rope(x[:, :Hq + H], y[:, :Hq + H], pos, freq, "interleaved", 1.0, "forward", "rope in place")
+    assert same_bits(y[:, Hq + H:], x[:, Hq + H:])          # the values' slice stays
+
+
+def test_rope_head_major_cache_and_odd_element_alignment(hk):
+    H, T, D = 3, 50, 64
+    buf = torch.randn(1 + H * T * D, generator=gen_of(3)).to(torch.bfloat16).cuda()
+    k = buf[1:].view(H, T, D).transpose(0, 1)               # 2-byte aligned, [H, T, D] in memory
+    out = torch.zeros_like(buf)[1:].view(H, T, D).transpose(0, 1)
+    pos = torch.arange(T, dtype=torch.int32)
+    hk.helm_rope(None, k, pos.cuda(), rope_plan(hk, D, D, "half", "plain"), hk.HELM_ROPE_INVERSE, out_k=out)
+    check_rope(k.cpu(), out, pos, ref.rope_frequencies(D, 1e6), "half", 1.0, "inverse", "rope cache")
+
+
+def test_rope_adjoint_is_the_gradient(hk):
+    """Against the derivative of the plain formula, and against differences of the call itself."""
+    N, H, D, rot = 5, 2, 64, 48
+    g = gen_of(4)
+    plan = rope_plan(hk, D, rot, "half", "yarn", factor=8.0, original_len=2048.0)
+    freq, m = ref.rope_frequencies(rot, 1e6, "yarn", 8.0, 2048.0), 0.1 * math.log(8.0) + 1.0
+    x = torch.randn((N, H, D), generator=g)
+    dy, step = torch.randn((N, H, D), generator=g), torch.randn((N, H, D), generator=g)
+    pos = torch.randint(0, 9000, (N,), generator=g).to(torch.int32)
+    leaf = x.double().requires_grad_()
+    P = rot // 2
+    ang = pos.double()[:, None, None] * freq
+    a, b = leaf[..., :P], leaf[..., P:rot]
+    y = torch.cat((m * (a * ang.cos() - b * ang.sin()), m * (a * ang.sin() + b * ang.cos()), leaf[..., rot:]), -1)
+    y.backward(dy.double())
+    _, dx = hk.helm_rope(None, dy.cuda(), pos.cuda(), plan, hk.HELM_ROPE_ADJOINT)
+    _, size = ref.rope(dy, pos, freq, "half", m, "adjoint")
+    within(dx, leaf.grad, (11 * 2.0 ** -24 + 2.0 ** -52 * 9000) * size, "rope gradient")
+    # <dy, f(x + h) - f(x - h)> = 2 <f^T dy, h>: the map is linear, so differences are exact but for roundings
+    plus, minus = (hk.helm_rope(None, (x + s * step).cuda(), pos.cuda(), plan)[1].double().cpu() for s in (1, -1))
+    lhs, rhs = float((dy.double() * (plus - minus)).sum()), 2 * float((dx.double().cpu() * step.double()).sum())
+    room = 40 * 2.0 ** -24 * m * float((dy.double().abs() * 2).sum() * (x.abs().max() + step.abs().max()))
+    assert abs(lhs - rhs) <= room, (lhs, rhs, room)
+
+
+# ------------------------------------------------------------ the store
+def run_store(hk, c, x, cu, start, max_len, weights=None, transpose=False):
+    d = {n: t.cuda() for n, t in c.items()}
+    k, v = (t.transpose(0, 1).contiguous().cuda().transpose(0, 1) if transpose else t.cuda() for t in x)
+    shape = hk.make_kv8_shape(d["k_pool"], d["table"], x[0].shape[0], max_kv_len=max_len)
+    w = None if weights is None else weights.cuda()
+    hk.helm_kv8_store(k, v, i32(cu).cuda(), i32(start).cuda(), d["table"], d["k_pool"], d["v_pool"], d["k_scale"],
+                      d["v_scale"], shape, weights=w)
+    return d, w
+
+
+@pytest.mark.parametrize("B,H,D,starts,news,dtype,transpose", [
+    (16, 2, 128, [5, 0, 16, 31], [1, 1, 1, 1], torch.bfloat16, False),
+    (16, 1, 64, [3, 0, 40, 7], [0, 50, 17, 9], torch.float32, True),
+    (48, 3, 64, [47, 48, 10], [2, 100, 1], torch.bfloat16, True),
+    (256, 1, 128, [200, 0], [300, 1], torch.bfloat16, False),
+    (32, 8, 128, [0], [1000], torch.bfloat16, True)])
+def test_store(hk, B, H, D, starts, news, dtype, transpose):
+    g = gen_of(B + D + sum(news))
+    lens = [a + b for a, b in zip(starts, news)]
+    c = ref.cache(g, lens, B, H, D)
+    cu = ref.cumulative(news)
+    # sizes over many powers of two, so that some blocks grow their scale and some keep it
+    x = [(torch.randn((cu[-1], H, D), generator=g) * torch.exp2(torch.randint(-12, 9, (cu[-1], H, 1), generator=g)
+                                                              .float())).to(dtype) for _ in range(2)]
+    weights = torch.rand((c["k_pool"].shape[0], H, B), generator=g)
+    d, w = run_store(hk, c, x, cu, starts, max(lens), weights, transpose)
+    expect = weights.clone()
+    for i, n in enumerate(("k", "v")):
+        for blk, a, b in ref.store(x[i], c[n + "_pool"], c[n + "_scale"], cu, starts, c["table"], max(lens)):
+            expect[blk, :, a:b] = 0
+        assert same_bits(d[n + "_scale"], c[n + "_scale"]), n
+        assert same_bits(d[n + "_pool"], c[n + "_pool"]), n
+    assert same_bits(w, expect)
+
+
+def test_store_odd_values(hk):
+    """Zeros, the smallest and largest numbers, infinities and NaN."""
+    B, H, D = 16, 1, 64
+    c = ref.cache(gen_of(9), [16 * 6], B, H, D)
+    x = torch.randn((16 * 6, H, D), generator=gen_of(10))
+    x[0:16] = 0.0
+    x[16:32] *= 1e-41                               # subnormal
+    x[32:48] *= 2.0 ** 100
+    x[48, 0, 3], x[49, 0, 5], x[50, 0, 7] = math.inf, -math.inf, math.nan
+    x[64:80] = math.inf
+    x[80, 0] = 448.0 * 2.0 ** -3                    # exactly the largest code
+    x[81:96] = 0.0
+    d, _ = run_store(hk, c, [x, -x], [0, 96], [0], 96)
+    for i, n in enumerate(("k", "v")):
+        y = x if i == 0 else -x
+        ref.store(y, c[n + "_pool"], c[n + "_scale"], [0, 96], [0], c["table"], 96)
+        assert same_bits(d[n + "_scale"], c[n + "_scale"]), n
+        a, b = d[n + "_pool"].cpu().float(), c[n + "_pool"].float()     # a NaN's sign is free
+        assert torch.equal(a.isnan(), b.isnan()) and torch.equal(a.nan_to_num(), b.nan_to_num()), n
+
+
+def test_store_in_steps_agrees_with_one_call(hk):
+    """Power-of-two scales: a block grown token by token holds what one call gives, but for codes below
+    e4m3's normal range, which round twice."""
+    B, H, D, n = 16, 2, 64, 40
+    x = torch.randn((n, H, D), generator=gen_of(11)).to(torch.bfloat16)
+    c = ref.cache(gen_of(12), [n], B, H, D)
+    one, _ = run_store(hk, c, [x, x], [0, n], [0], n)
+    step = {k: t.cuda() for k, t in c.items()}
+    for t in range(n):
+        shape = hk.make_kv8_shape(step["k_pool"], step["table"], 1, max_kv_len=n)
+        y = x[t:t + 1].cuda()
+        hk.helm_kv8_store(y, y, i32([0, 1]).cuda(), i32([t]).cuda(), step["table"], step["k_pool"], step["v_pool"],
+                          step["k_scale"], step["v_scale"], shape)
+    assert same_bits(one["k_scale"], step["k_scale"])
+    full = [p["k_pool"].cpu().float() * p["k_scale"].cpu()[..., None, None] for p in (one, step)]
+    tiny = 2.0 ** -9 * one["k_scale"].cpu()[..., None, None]            # e4m3's smallest step
+    blocks = c["table"][0, :2].long()                                    # full pages: the rest holds NaN slots
+    assert bool(((full[0] - full[1]).abs() <= tiny)[blocks].all())
+
+
+def test_store_skips_absent_pages_and_tokens_past_the_bound(hk):
+    B, H, D = 16, 1, 64
+    c = ref.cache(gen_of(13), [64, 64], B, H, D)
+    c["table"][0, 1], c["table"][1, 2] = -1, c["k_pool"].shape[0] + 5
+    x = [torch.randn((128, H, D), generator=gen_of(14 + i)).to(torch.bfloat16) for i in range(2)]
+    d, _ = run_store(hk, c, x, [0, 64, 128], [0, 0], 50)
+    for i, n in enumerate(("k", "v")):
+        ref.store(x[i], c[n + "_pool"], c[n + "_scale"], [0, 64, 128], [0, 0], c["table"], 50)
+        assert same_bits(d[n + "_pool"], c[n + "_pool"]) and same_bits(d[n + "_scale"], c[n + "_scale"])
+
+
+# ------------------------------------------------------------ attention and the weight it gives
+CASES = [
+    # B, H, G, D, kv, new, causal, window
+    (16, 2, 1, 128, [1], [1], True, 0),
+    (16, 2, 5, 128, [17, 1, 33, 512], [1, 1, 1, 1], True, 0),
+    (48, 1, 8, 64, [100, 47, 48, 49], [1, 1, 1, 1], True, 0),
+    (16, 3, 7, 64, [0, 5, 2000], [0, 0, 1], True, 0),                  # requests with nothing to do
+    (32, 1, 16, 128, [3000], [1], True, 0),                            # a split context
+    (16, 2, 8, 128, [700, 40], [4, 4], True, 0),                       # rows over one tile
+    (16, 1, 20, 64, [90, 300], [1, 1], True, 0),                       # a group over one tile
+    (16, 2, 2, 128, [5, 64, 3], [9, 64, 3], True, 0),                  # queries before the first token see nothing
+    (256, 2, 3, 64, [333, 600], [70, 129], True, 0),
+    (32, 2, 2, 128, [257, 96], [100, 96], False, 0),
+    (16, 2, 4, 128, [1000, 37], [1, 1], True, 100),
+    (16, 1, 2, 64, [513, 200], [150, 33], True, 7),
+    (64, 1, 1, 128, [260], [260], True, 0),
+    (16, 8, 5, 128, [1500, 1], [300, 1], True, 0)]
+
+
+def attend_inputs(B, H, G, D, kv, new, seed):
+    g = gen_of(seed)
+    c = ref.cache(g, kv, B, H, D, width=max(1, -(-max(kv) // B)))
+    q = (torch.randn((sum(new), H * G, D), generator=g) * 1.5).to(torch.bfloat16)
+    return c, q, ref.cumulative(new)
+
+
+def run_attend(hk, c, q, cu, kv, causal=True, window=0, max_len=None, **kw):
+    d = {n: t.cuda() for n, t in c.items()}
+    max_len = max(kv) if max_len is None else max_len
+    shape = hk.make_kv8_shape(d["k_pool"], d["table"], q.shape[0], n_q_heads=q.shape[1], max_kv_len=max_len,
+                              causal=causal, window=window)
+    out, lse = hk.helm_kv8_attend(q if q.is_cuda else q.cuda(), i32(cu).cuda(), i32(kv).cuda(), d["table"],
+                                  d["k_pool"], d["v_pool"], d["k_scale"], d["v_scale"], shape, **kw)
+    return d, shape, out, lse
+
+
+@pytest.mark.parametrize("B,H,G,D,kv,new,causal,window", CASES)
+def test_attend_and_weigh(hk, B, H, G, D, kv, new, causal, window):
+    c, q, cu = attend_inputs(B, H, G, D, kv, new, 31 * B + sum(kv))
+    d, shape, out, lse = run_attend(hk, c, q, cu, kv, causal, window)
+    args = (cu, kv, c["table"])
+    o, z, t_o, t_z = ref.attend(q, *args, c["k_pool"], c["v_pool"], c["k_scale"], c["v_scale"], max(kv), D ** -0.5,
+                                causal, window)
+    within(out, o, t_o, "attend out")
+    within(lse, z, t_z, "attend lse")
+    w0 = torch.rand((c["k_pool"].shape[0], H, B), generator=gen_of(5))
+    w = w0.cuda()
+    for _ in range(2):      # weights accumulate
+        hk.helm_kv8_weigh(q.cuda(), lse, i32(cu).cuda(), i32(kv).cuda(), d["table"], d["k_pool"], d["k_scale"], w, shape)
+    once, tol = ref.weigh(q, lse.cpu(), *args, c["k_pool"], c["k_scale"], w0, max(kv), D ** -0.5, causal, window)
+    within(w, 2 * once - w0.double(), 2 * tol, "weigh")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_strided_queries_on_another_stream(hk, D):
+    B, H, G, kv, new = 16, 2, 3, [200, 77], [3, 1]
+    c, q, cu = attend_inputs(B, H, G, D, kv, new, 77)
+    fused = torch.zeros((4, H * G + 3, D + 1), dtype=torch.bfloat16, device="cuda")
+    view = fused[:, 1:1 + H * G, 1:]                        # 2-byte aligned heads, odd strides
+    view.copy_(q.cuda())
+    _, _, want, want_lse = run_attend(hk, c, q, cu, kv)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        _, _, out, lse = run_attend(hk, c, view, cu, kv)
+    s.synchronize()
+    assert same_bits(out, want) and same_bits(lse, want_lse)
+
+
+def test_attend_absent_pages_and_lengths_past_the_bound(hk):
+    B, H, G, D, kv, new = 16, 2, 4, 128, [160, 200], [1, 40]
+    c, q, cu = attend_inputs(B, H, G, D, kv, new, 88)
+    c["table"][0, 3], c["table"][0, 9], c["table"][1, 0] = -1, 10 ** 6, -7
+    d, shape, out, lse = run_attend(hk, c, q, cu, kv, max_len=190)
+    o, z, t_o, t_z = ref.attend(q, cu, kv, c["table"], c["k_pool"], c["v_pool"], c["k_scale"], c["v_scale"], 190,
+                                D ** -0.5)
+    within(out, o, t_o, "absent out")
+    within(lse, z, t_z, "absent lse")
+    w = torch.zeros((c["k_pool"].shape[0], H, B), device="cuda")
+    hk.helm_kv8_weigh(q.cuda(), lse, i32(cu).cuda(), i32(kv).cuda(), d["table"], d["k_pool"], d["k_scale"], w, shape)
+    want, tol = ref.weigh(q, lse.cpu(), cu, kv, c["table"], c["k_pool"], c["k_scale"], w.cpu() * 0, 190, D ** -0.5)
+    within(w, want, tol, "absent weigh")
+
+
+@pytest.mark.parametrize("new", [1, 50])
+def test_attend_peaked_scores_and_scales_of_any_size(hk, new):
+    """Scores up to +-1e4 (the running maximum moves), scales that are no powers of two."""
+    B, H, G, D, kv = 16, 1, 4, 128, [900]
+    c, q, cu = attend_inputs(B, H, G, D, kv, [new], 99)
+    c["k_scale"] = torch.rand(c["k_scale"].shape, generator=gen_of(6)) * 3
+    c["v_scale"] = torch.exp2(torch.randint(-60, 60, c["v_scale"].shape, generator=gen_of(7)).float()) * 1.3
+    _, _, out, lse = run_attend(hk, c, q, cu, kv)
+    o, z, t_o, t_z = ref.attend(q, cu, kv, c["table"], c["k_pool"], c["v_pool"], c["k_scale"], c["v_scale"], 900,
+                                D ** -0.5)
+    within(out, o, t_o, "peaked out")
+    within(lse, z, t_z, "peaked lse")
+
+
+def test_attend_pool_offsets_past_32_bits(hk):
+    B, H, G, D, n = 16, 8, 5, 128, 200
+    nb = (1 << 32) // (H * B * D) + 64
+    blocks = list(range(nb - 13, nb))
+    c, q, cu = attend_inputs(B, H, G, D, [n], [1], 111)
+    k_pool = torch.empty((nb, H, B, D), dtype=torch.uint8, device="cuda").view(ref.FP8)
+    v_pool = torch.empty((nb, H, B, D), dtype=torch.uint8, device="cuda").view(ref.FP8)
+    k_scale, v_scale = (torch.empty((nb, H), device="cuda") for _ in range(2))
+    table = i32([blocks]).cuda()
+    x = [torch.randn((n, H, D), generator=gen_of(8 + i)).to(torch.bfloat16) for i in range(2)]
+    st = hk.make_kv8_shape(k_pool, table, n, max_kv_len=n)
+    hk.helm_kv8_store(x[0].cuda(), x[1].cuda(), i32([0, n]).cuda(), i32([0]).cuda(), table, k_pool, v_pool, k_scale,
+                      v_scale, st)
+    shape = hk.make_kv8_shape(k_pool, table, 1, n_q_heads=H * G, max_kv_len=n)
+    out, lse = hk.helm_kv8_attend(q.cuda(), i32(cu).cuda(), i32([n]).cuda(), table, k_pool, v_pool, k_scale, v_scale,
+                                  shape)
+    small = dict(table=i32([range(13)]), k_pool=k_pool[-13:].cpu(), v_pool=v_pool[-13:].cpu(),
+                 k_scale=k_scale[-13:].cpu(), v_scale=v_scale[-13:].cpu())
+    o, z, t_o, t_z = ref.attend(q, cu, [n], small["table"], small["k_pool"], small["v_pool"], small["k_scale"],
+                                small["v_scale"], n, D ** -0.5)
+    within(out, o, t_o, "far pool out")
+    within(lse, z, t_z, "far pool lse")
+
+
+# ------------------------------------------------------------ eviction
+@pytest.mark.parametrize("B,H,D,kv,budget,recent", [
+    (16, 2, 128, [100, 16, 17, 0, 1], 16, 4),
+    (16, 1, 64, [5000], 700, 0),
+    (48, 2, 64, [333, 47, 2100], 333, 333),              # only recent ones
+    (32, 3, 128, [1500, 200], 1, 0),
+    (16, 2, 64, [1024, 1025, 2049], 1024, 100)])
+def test_evict(hk, B, H, D, kv, budget, recent):
+    g = gen_of(B + budget + sum(kv))
+    c = ref.cache(g, kv, B, H, D, spare=len(kv) * -(-budget // B) + 2)
+    nb = c["k_pool"].shape[0]
+    used = set(c["table"][c["table"] >= 0].tolist())
+    free = [b for b in range(nb) if b not in used]
+    M = -(-budget // B)
+    dst = i32([free[r * M:(r + 1) * M] for r in range(len(kv))])
+    # few distinct weights, so that ties reach over the threshold; zeros of both signs, one NaN
+    weights = torch.randint(0, 40, (nb, H, B), generator=g).float() / 8
+    weights[weights == 0] = -0.0
+    weights[::2][weights[::2] == 0] = 0.0
+    if kv[0]:
+        weights[int(c["table"][0, 0]), :, 0] = math.nan
+    d = {n: t.cuda() for n, t in c.items()}
+    shape = hk.make_kv8_evict_shape(d["k_pool"], d["table"], dst, budget, recent, max_kv_len=max(kv))
+    assert hk.helm_kv8_evict_check(shape, kv, c["table"], dst) == 0, hk.helm_last_error()
+    w = weights.cuda()
+    kept, new_len = hk.helm_kv8_evict(w, i32(kv).cuda(), d["table"], dst.cuda(), d["k_pool"], d["v_pool"],
+                                      d["k_scale"], d["v_scale"], shape)
+    want, lens = ref.evict(weights, kv, c["table"], dst, c["k_pool"], c["v_pool"], c["k_scale"], c["v_scale"], budget,
+                           recent, max(kv))
+    assert torch.equal(new_len.cpu(), lens) and torch.equal(kept.cpu(), want)
+    assert same_bits(w, weights)
+    for n in ("k_scale", "v_scale", "k_pool", "v_pool"):
+        assert same_bits(d[n], c[n]), n
+
+
+def test_evict_absent_pages_go_first(hk):
+    B, H, D, kv = 16, 1, 64, [96]
+    c = ref.cache(gen_of(15), kv, B, H, D, spare=4)
+    nb = c["k_pool"].shape[0]
+    free = [b for b in range(nb) if b not in c["table"][0].tolist()]
+    c["table"][0, 2] = nb
+    dst = i32([[free[0], -1, free[1]]])
+    weights = torch.rand((nb, H, B), generator=gen_of(16))
+    d = {n: t.cuda() for n, t in c.items()}
+    shape = hk.make_kv8_evict_shape(d["k_pool"], d["table"], dst, 40, 3)
+    w = weights.cuda()
+    kept, _ = hk.helm_kv8_evict(w, i32(kv).cuda(), d["table"], dst.cuda(), d["k_pool"], d["v_pool"], d["k_scale"],
+                                d["v_scale"], shape)
+    want, _ = ref.evict(weights, kv, c["table"], dst, c["k_pool"], c["v_pool"], c["k_scale"], c["v_scale"], 40, 3, 96)
+    assert torch.equal(kept.cpu(), want) and same_bits(w, weights)
+    assert same_bits(d["k_pool"], c["k_pool"]) and same_bits(d["v_scale"], c["v_scale"])
+
+
+# ------------------------------------------------------------ together, in a graph
+def test_decode_step_in_a_graph(hk):
+    """rope -> store -> attend -> weigh of one token each for three requests, captured once and replayed: every
+    replay equals the eager calls on the same state."""
+    B, H, G, D, kv = 16, 2, 4, 128, [300, 16, 1025]
+    c, q, cu = attend_inputs(B, H, G, D, kv, [1, 1, 1], 123)
+    x = torch.randn((3, H * G + 2 * H, D), generator=gen_of(17)).to(torch.bfloat16).cuda()
+    plan = rope_plan(hk, D, D, "half", "yarn", factor=4.0, original_len=32768.0)
+    base = {n: t.cuda() for n, t in c.items()}
+    base["weights"] = torch.rand((c["k_pool"].shape[0], H, B), generator=gen_of(18)).cuda()
+    state = {n: t.clone() for n, t in base.items()}
+    cu_d, kv_d, start = i32(cu).cuda(), i32(kv).cuda(), (i32(kv) - 1).cuda()
+    st = hk.make_kv8_shape(base["k_pool"], base["table"], 3, n_q_heads=H * G, max_kv_len=max(kv))
+    bufs = dict(q=torch.empty((3, H * G, D), dtype=torch.bfloat16, device="cuda"),
+                k=torch.empty((3, H, D), dtype=torch.bfloat16, device="cuda"),
+                out=torch.empty((3, H * G, D), dtype=torch.bfloat16, device="cuda"),
+                lse=torch.empty((3, H * G), device="cuda"))
+    ws = torch.empty(hk.helm_kv8_attend_workspace_bytes(st), dtype=torch.uint8, device="cuda")
+
+    def step(s, b):
+        hk.helm_rope(x[:, :H * G], x[:, H * G:H * G + H], start, plan, out_q=b["q"], out_k=b["k"])
+        pools = (s["k_pool"], s["v_pool"], s["k_scale"], s["v_scale"])
+        hk.helm_kv8_store(b["k"], x[:, H * G + H:], cu_d, start, s["table"], *pools, st, weights=s["weights"])
+        hk.helm_kv8_attend(b["q"], cu_d, kv_d, s["table"], *pools, st, out=b["out"], lse=b["lse"], workspace=ws)
+        hk.helm_kv8_weigh(b["q"], b["lse"], cu_d, kv_d, s["table"], s["k_pool"], s["k_scale"], s["weights"], st)
+
+    step({n: t.clone() for n, t in base.items()}, {n: t.clone() for n, t in bufs.items()})      # warm
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(state, bufs)
+    for i in range(3):
+        x.copy_(torch.randn(x.shape, generator=gen_of(20 + i)).to(torch.bfloat16))
+        for n in base:
+            state[n].copy_(base[n])
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = {n: t.clone() for n, t in base.items()}
+        fresh = {n: torch.zeros_like(t) for n, t in bufs.items()}
+        step(eager, fresh)
+        torch.cuda.synchronize()
+        for n in eager:
+            assert same_bits(state[n], eager[n]), (i, n)
+        for n in fresh:
+            assert same_bits(bufs[n], fresh[n]), (i, n)
