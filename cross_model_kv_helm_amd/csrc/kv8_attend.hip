@@ -32,6 +32,9 @@
 namespace helm {
 namespace {
 
+#ifndef FILL
+#define FILL 768
+#endif
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -101,12 +104,14 @@ __device__ __forceinline__ Tile tile_at(const Kv8Cache& c, const int32_t* row, i
   return x;
 }
 
-// Keys of a tile: this lane's D/4 codes.
+// Keys of a tile: this lane's D/4 codes.  (A uniform base and a 32-bit lane
+// offset: one address register.)
 template <int D>
 __device__ __forceinline__ void load_k(const Kv8Cache& c, const Tile& x, int g, int m, u32x4 (&w)[D / 64]) {
-  const uint8_t* p = c.k_pool + (x.slab * c.B + x.off) * D + m * D + g * (D / 4);
+  const uint8_t* p = c.k_pool + (x.slab * c.B + x.off) * D;
+  const uint32_t lane = m * D + g * (D / 4);
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i) w[i] = *(const u32x4*)(p + 16 * i);
+  for (int i = 0; i < D / 64; ++i) w[i] = *(const u32x4*)(p + lane + 16 * i);
 }
 
 // 16 queries as the right operand of S^T: this lane's row, d = g*D/4 + 8s.
@@ -145,38 +150,162 @@ __device__ __forceinline__ Seen seen_by(const Kv8AttendArgs& a, const Request& q
 }
 
 // ---- attention ------------------------------------------------------------
-// One workgroup: 16*MT rows of one request and KV head over one piece of its
-// context; its waves take 32 tokens in turn and join at the end.
-template <int D, int MT>
-__global__ void __launch_bounds__(kThreads) kv8_attend_kernel(Kv8AttendArgs a) {
-  constexpr int TR = 16 * MT, NJ = D / 16, PAD = D + 4;
-  __shared__ float lds_o[kWaves][TR][PAD];
-  __shared__ float lds_m[kWaves][TR], lds_l[kWaves][TR];
+// An item is a row tile (16*MT*RG rows of one request) of one KV head.  A
+// workgroup works through one item's context, or a stretch of it: the
+// kWaves / RG = TG waves of a row group take 32 tokens in turn and join at the
+// end.
+//
+// A wave's step: S^T of the codes in w.k, the next keys into w.k, the softmax,
+// O^T with the codes in w.v, the next values into w.v: each load has the rest of
+// a step to arrive, with one buffer, and the block numbers are read two steps
+// ahead so that no load waits for its address.
+template <int D>
+struct Codes {
+  u32x4 k[2][D / 64];
+  uint32_t v[2][4][D / 64];
+};
+struct Pages {       // where two 16-token tiles are, and their scales
+  Tile x[2];
+  float ks[2], vs[2];
+};
+
+template <int D>
+__device__ __forceinline__ void load_v(const Kv8Cache& c, const Tile& x, int g, int m, uint32_t (&w)[4][D / 64]) {
+  const uint8_t* p = c.v_pool + (x.slab * c.B + x.off) * D;
+  const uint32_t lane = 4 * g * D + m * (D / 16);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (D == 128) {
+      const u32x2 v = *(const u32x2*)(p + lane + i * D);
+      w[i][0] = v[0];
+      w[i][1] = v[1];
+    } else {
+      w[i][0] = *(const uint32_t*)(p + lane + i * D);
+    }
+  }
+}
+
+// One row tile's probabilities (times the value's scale) of 32 tokens from
+// their raw scores; rescales l and o where the reference moves.
+template <int D, bool MASK>
+__device__ __forceinline__ bf16x8 probabilities(const f32x4 (&s)[2], const float (&ks)[2], const float (&lv)[2],
+                                                const float (&inv)[2], const Seen& see, int tok, float& mref, float& l,
+                                                f32x4 (&o)[D / 16]) {
+  float y[8], top[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    if constexpr (MASK) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = tok + 16 * u + i;
+        y[4 * u + i] = t < see.lo || t >= see.hi ? -INFINITY : s[u][i] * ks[u];
+      }
+      top[u] = fmaxf(fmaxf(y[4 * u], y[4 * u + 1]), fmaxf(y[4 * u + 2], y[4 * u + 3]));
+    } else {
+      top[u] = fmaxf(fmaxf(s[u][0], s[u][1]), fmaxf(s[u][2], s[u][3])) * ks[u];
+    }
+  }
+  float t = fmaxf(top[0], top[1]);
+  if (__any(t > mref + kLazy)) {
+    t = fmaxf(t, __shfl_xor(t, 16));
+    t = fmaxf(t, __shfl_xor(t, 32));
+    t = fmaxf(t, mref);
+    const float shrink = exp2f(mref - t);
+    mref = t;
+    l *= shrink;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) o[j] *= shrink;
+  }
+  bf16x8 p;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const float down = lv[u] - mref;
+    float e[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      e[i] = __builtin_amdgcn_exp2f(MASK ? y[4 * u + i] + down : fmaf(s[u][i], ks[u], down));
+      p[4 * u + i] = (__bf16)e[i];
+    }
+    l = fmaf((e[0] + e[1]) + (e[2] + e[3]), inv[u], l);
+  }
+  return p;
+}
+
+// A stretch of an item's context, uniform over the workgroup.
+struct Stretch {
+  int h, tile;       // KV head, row tile of the request
+  int from, to;      // tokens [from, to), from a multiple of 16
+  int64_t piece;     // < 0: the whole context, results are final; else where its sums go
+};
+// The workspace: per piece the (m, l) of its rows, behind them all the D sums
+// of each row.
+__device__ __forceinline__ float* piece_ml(const Kv8AttendArgs& a, int64_t piece, int row) {
+  return a.part + (piece * a.row_tile + row) * 2;
+}
+__device__ __forceinline__ float* piece_sums(const Kv8AttendArgs& a, int64_t piece, int row) {
+  return a.part + (int64_t)a.pieces * a.row_tile * 2 + (piece * a.row_tile + row) * a.c.D;
+}
+
+// A row of an item, D/16 values a lane and i: final, or one piece's.
+template <int D>
+__device__ __forceinline__ void write_row(const Kv8AttendArgs& a, int64_t at, int64_t piece, int row, int g, float top,
+                                          float sum, const f32x4 (&o)[D / 16]) {
+  if (piece >= 0) {
+    if (g == 0) *(f32x2*)piece_ml(a, piece, row) = f32x2{top, sum};
+    float* v = piece_sums(a, piece, row) + g * (D / 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int b = 0; b < D / 64; ++b)
+        *(f32x4*)(v + (D / 16) * i + 4 * b) = f32x4{o[4 * b][i], o[4 * b + 1][i], o[4 * b + 2][i], o[4 * b + 3][i]};
+    return;
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // a row that sees nothing: 0
+  uint16_t* y = a.out + at * D + g * (D / 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int b = 0; b < D / 64; ++b) {
+      const bf16x2 lo = {(__bf16)(o[4 * b][i] * inv), (__bf16)(o[4 * b + 1][i] * inv)};
+      const bf16x2 hi = {(__bf16)(o[4 * b + 2][i] * inv), (__bf16)(o[4 * b + 3][i] * inv)};
+      *(u32x2*)(y + (D / 16) * i + 4 * b) = u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+    }
+  if (g == 0) a.lse[at] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
+template <int D, int MT, int RG>
+struct AttendLds {
+  static constexpr int TG = kWaves / RG, PAD = D + 4;
+  static constexpr int kJoinRows = TG == 4 ? 16 * MT : TG == 2 ? 8 * MT : 1;   // of a wave, exchanged at the end
+  float o[kWaves][kJoinRows][PAD];
+  float m[kWaves][16 * MT], l[kWaves][16 * MT];
+};
+
+template <int D, int MT, int RG>
+__device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Request& q, const Stretch& st,
+                                               AttendLds<D, MT, RG>& lds) {
+  constexpr int TG = kWaves / RG, TR = 16 * MT * RG, NJ = D / 16, KS = D / 32;
   const Kv8Cache& c = a.c;
-  const int split = blockIdx.x % a.splits;
-  const int th = blockIdx.x / a.splits;
-  const int h = th % c.H;
-  int64_t base;
-  const int r = owner_of(a.cu, c.R, a.n_tok, a.G, TR, 1, th / c.H, base);
-  const Request q = request_at(a, r);
+  const int h = st.h;
   const int M = q.n * a.G;
-  const int64_t first = (th / c.H - base) * TR;
-  if (first >= M) return;
-  const int row0 = (int)first;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rg = wave / TG, tg = wave % TG;
+  const int row0 = st.tile * TR, rowg = row0 + 16 * MT * rg;      // the workgroup's, this wave's
   const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
 
-  bf16x8 qv[MT][D / 32];
+  bf16x8 qv[MT][KS];
   Seen see[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
-    const int row = min(row0 + 16 * t + m, M - 1);
-    load_q<D>(a, q, h, row, g, qv[t]);
+    const int row = min(rowg + 16 * t + m, M - 1);
     see[t] = seen_by(a, q, row / a.G);
+    load_q<D>(a, q, h, row, g, qv[t]);
   }
-  const Seen s_first = seen_by(a, q, row0 / a.G), s_last = seen_by(a, q, (min(row0 + TR, M) - 1) / a.G);
-  const int begin = (s_first.lo & ~15) + split * a.chunk;
-  const int end = min(s_last.hi, begin + a.chunk);
+  const int last = min(rowg + 16 * MT, M) - 1;
+  const Seen s_first = seen_by(a, q, min(rowg, M - 1) / a.G), s_last = seen_by(a, q, last / a.G);
+  // a wave of a row group that has no rows left (rowg >= M) finds begin >= end
+  const int begin = max(st.from, s_first.lo & ~15);
+  const int end = rowg < M ? min(s_last.hi, st.to) : 0;
 
   f32x4 o[MT][NJ];
   float mref[MT], l[MT];
@@ -189,97 +318,98 @@ __global__ void __launch_bounds__(kThreads) kv8_attend_kernel(Kv8AttendArgs a) {
   }
 
   const int32_t* table = c.table + (int64_t)q.r * c.max_blocks;
-  for (int t0 = begin + wave * kStep; t0 < end; t0 += kWaves * kStep) {
-    Tile x[2];
-    u32x4 kw[2][D / 64];
-    uint32_t vw[2][4][D / 64];
-    float ks[2], vs[2];
-    bool odd = t0 + kStep > q.len;
+  const auto tiles = [&](int t, Tile (&x)[2]) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) x[u] = tile_at(c, table, h, t + 16 * u, min(end, q.len));
+  };
+  const auto scales = [&](const Tile (&x)[2], float (&ks)[2], float (&vs)[2]) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      x[u] = tile_at(c, table, h, t0 + 16 * u, q.len);
-      load_k<D>(c, x[u], g, m, kw[u]);
-      const uint8_t* p = c.v_pool + (x[u].slab * c.B + x[u].off + 4 * g) * D + m * (D / 16);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (D == 128) {
-          const u32x2 v = *(const u32x2*)(p + i * D);
-          vw[u][i][0] = v[0];
-          vw[u][i][1] = v[1];
-        } else {
-          vw[u][i][0] = *(const uint32_t*)(p + i * D);
-        }
-      }
       ks[u] = c.k_scale[x[u].slab] * a.scale_log2;
       vs[u] = c.v_scale[x[u].slab];
-      odd |= !x[u].ok || !(vs[u] > 0.0f);
+    }
+  };
+  constexpr int kStride = TG * kStep;
+  int t0 = begin + tg * kStep;
+  Codes<D> w;
+  Pages now, next;
+  Tile after[2];
+  tiles(t0, now.x);
+  tiles(t0 + kStride, next.x);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) load_k<D>(c, now.x[u], g, m, w.k[u]);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) load_v<D>(c, now.x[u], g, m, w.v[u]);
+  scales(now.x, now.ks, now.vs);
+
+  for (; t0 < end; t0 += kStride) {
+    f32x4 s[MT][2];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) s[t][0] = s[t][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      bf16x8 k[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) k[u] = cvt8(w.k[u][i / 2][2 * (i & 1)], w.k[u][i / 2][2 * (i & 1) + 1]);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        s[t][0] = mfma(k[0], qv[t][i], s[t][0]);
+        s[t][1] = mfma(k[1], qv[t][i], s[t][1]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) load_k<D>(c, next.x[u], g, m, w.k[u]);
+    scales(next.x, next.ks, next.vs);
+    tiles(t0 + 2 * kStride, after);
+
+    float lv[2], inv[2];
+    bool odd = t0 + kStep > q.len, there = true;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      there = there && now.x[u].ok;
+      odd = odd || !now.x[u].ok || !(now.vs[u] > 0.0f);
     }
     // tokens past the context are not read as numbers: their codes may be anything
     if (odd) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const bool none = !x[u].ok || !(vs[u] > 0.0f);
-        if (none) vs[u] = 1.0f;
+        const bool none = !now.x[u].ok || !(now.vs[u] > 0.0f);
+        if (none) now.vs[u] = 1.0f;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (none || t0 + 16 * u + 4 * g + i >= q.len) {
 #pragma unroll
-            for (int b = 0; b < D / 64; ++b) vw[u][i][b] = 0u;
+            for (int b = 0; b < D / 64; ++b) w.v[u][i][b] = 0u;
           }
       }
     }
-    float lv[2], inv[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      lv[u] = __builtin_amdgcn_logf(vs[u]);
-      inv[u] = __builtin_amdgcn_rcpf(vs[u]);
+      lv[u] = __builtin_amdgcn_logf(now.vs[u]);
+      inv[u] = __builtin_amdgcn_rcpf(now.vs[u]);
     }
-    const bool all_seen = t0 >= s_last.lo && t0 + kStep <= s_first.hi && x[0].ok && x[1].ok;
-
     bf16x8 pv[MT];
+    if (t0 >= s_last.lo && t0 + kStep <= s_first.hi && there) {
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      float y[8];
+      for (int t = 0; t < MT; ++t)
+        pv[t] = probabilities<D, false>(s[t], now.ks, lv, inv, see[t], 0, mref[t], l[t], o[t]);
+    } else {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const f32x4 s = scores<D>(kw[u], qv[t]);
+      for (int u = 0; u < 2; ++u)
+        if (!now.x[u].ok) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[4 * u + i] = fmaf(s[i], ks[u], lv[u]);
-      }
-      if (!all_seen) {
+          for (int t = 0; t < MT; ++t) s[t][u] = f32x4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          now.ks[u] = 1.0f;
+        }
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int tok = t0 + 16 * u + 4 * g + i;
-            if (!x[u].ok || tok < see[t].lo || tok >= see[t].hi) y[4 * u + i] = -INFINITY;
-          }
-      }
-      const float top0 = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) - lv[0];
-      const float top1 = fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])) - lv[1];
-      float top = fmaxf(top0, top1);
-      if (__any(top > mref[t] + kLazy)) {
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        top = fmaxf(top, mref[t]);
-        const float shrink = exp2f(mref[t] - top);
-        mref[t] = top;
-        l[t] *= shrink;
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) o[t][j] *= shrink;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float p = __builtin_amdgcn_exp2f(y[i] - mref[t]);   // probability times the value's scale
-        l[t] = fmaf(p, inv[i >> 2], l[t]);
-        pv[t][i] = (__bf16)p;
-      }
+      for (int t = 0; t < MT; ++t)
+        pv[t] = probabilities<D, true>(s[t], now.ks, lv, inv, see[t], t0 + 4 * g, mref[t], l[t], o[t]);
     }
 #pragma unroll
     for (int b = 0; b < D / 64; ++b) {
       uint32_t w0[4], w1[4];
-      transpose4(vw[0][0][b], vw[0][1][b], vw[0][2][b], vw[0][3][b], w0);
-      transpose4(vw[1][0][b], vw[1][1][b], vw[1][2][b], vw[1][3][b], w1);
+      transpose4(w.v[0][0][b], w.v[0][1][b], w.v[0][2][b], w.v[0][3][b], w0);
+      transpose4(w.v[1][0][b], w.v[1][1][b], w.v[1][2][b], w.v[1][3][b], w1);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const bf16x8 v = cvt8(w0[j], w1[j]);
@@ -287,100 +417,262 @@ __global__ void __launch_bounds__(kThreads) kv8_attend_kernel(Kv8AttendArgs a) {
         for (int t = 0; t < MT; ++t) o[t][4 * b + j] = mfma(v, pv[t], o[t][4 * b + j]);
       }
     }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) load_v<D>(c, next.x[u], g, m, w.v[u]);
+    now = next;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) next.x[u] = after[u];
   }
 
-  // join the waves: lane (g, m) has row m, d = g*D/4 + (D/16)*i + j
+  // join the waves of a row group: lane (g, m) has row m, d = g*D/4 + (D/16)*i + j
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
     l[t] += __shfl_xor(l[t], 16);
     l[t] += __shfl_xor(l[t], 32);
-    if (g == 0) {
-      lds_m[wave][16 * t + m] = mref[t];
-      lds_l[wave][16 * t + m] = l[t];
-    }
+  }
+  const auto row_at = [&](int row) {
+    const int i = row / a.G;
+    return (q.c0 + i) * a.Hq + h * a.G + (row - i * a.G);
+  };
+  const auto put = [&](int t, int slot) {     // this wave's row tile t for the others
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int b = 0; b < D / 64; ++b)
-        *(f32x4*)&lds_o[wave][16 * t + m][g * (D / 4) + (D / 16) * i + 4 * b] =
+        *(f32x4*)&lds.o[wave][16 * slot + m][g * (D / 4) + (D / 16) * i + 4 * b] =
             f32x4{o[t][4 * b][i], o[t][4 * b + 1][i], o[t][4 * b + 2][i], o[t][4 * b + 3][i]};
-  }
-  __syncthreads();
-  const int64_t rows = a.n_tok * a.Hq;
-  for (int e = threadIdx.x; e < TR * (D / 4); e += kThreads) {
-    const int t = e / (D / 4), d = e % (D / 4) * 4, row = row0 + t;
-    if (row >= M) break;
-    float top = lds_m[0][t];
+  };
+  if constexpr (TG == 1) {
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) top = fmaxf(top, lds_m[w][t]);
-    float sum = 0.0f;
-    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int t = 0; t < MT; ++t)
+      if (rowg + 16 * t + m < M) 
+        write_row<D>(a, row_at(rowg + 16 * t + m), st.piece, rowg - row0 + 16 * t + m, g, mref[t], l[t], o[t]);
+  } else if constexpr (TG == 2) {   // each of the two finishes half of the row tiles
+    constexpr int HT = MT / 2;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const float f = exp2f(lds_m[w][t] - top);
-      sum += f * lds_l[w][t];
-      v += f * *(const f32x4*)&lds_o[w][t][d];
+    for (int t = 0; t < MT; ++t) {
+      if (g == 0) {
+        lds.m[wave][16 * t + m] = mref[t];
+        lds.l[wave][16 * t + m] = l[t];
+      }
+      if (t / HT != tg) put(t, t % HT);
     }
-    const int i = row / a.G;
-    const int64_t at = (q.c0 + i) * a.Hq + h * a.G + (row - i * a.G);
-    if (a.splits == 1) {
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // a row that sees nothing: 0
-      const bf16x2 lo = {(__bf16)(v[0] * inv), (__bf16)(v[1] * inv)}, hi = {(__bf16)(v[2] * inv), (__bf16)(v[3] * inv)};
-      const u32x2 w = {__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
-      *(u32x2*)(a.out + at * D + d) = w;
-      if (d == 0) a.lse[at] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
-    } else {
-      float* ml = a.part + ((int64_t)split * rows + at) * 2;
-      if (d == 0) *(f32x2*)ml = f32x2{top, sum};
-      if (sum != 0.0f)
-        *(f32x4*)(a.part + 2 * (int64_t)a.splits * rows + ((int64_t)split * rows + at) * D + d) = v;
+    __syncthreads();
+    const int other = wave ^ 1;
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const int row = rowg + 16 * t + m;
+      if (t / HT != tg || row >= M) continue;
+      const float mo = lds.m[other][16 * t + m], top = fmaxf(mref[t], mo);
+      const float f = exp2f(mref[t] - top), fo = exp2f(mo - top);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int b = 0; b < D / 64; ++b) {
+          const f32x4 v = *(const f32x4*)&lds.o[other][16 * (t % HT) + m][g * (D / 4) + (D / 16) * i + 4 * b];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[t][4 * b + j][i] = f * o[t][4 * b + j][i] + fo * v[j];
+        }
+      write_row<D>(a, row_at(row), st.piece, row - row0, g, top, f * l[t] + fo * lds.l[other][16 * t + m], o[t]);
+    }
+  } else {                          // few rows: all threads side by side over them
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      if (g == 0) {
+        lds.m[wave][16 * t + m] = mref[t];
+        lds.l[wave][16 * t + m] = l[t];
+      }
+      put(t, t);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < TR * (D / 4); e += kThreads) {
+      const int t = e / (D / 4), d = e % (D / 4) * 4, row = row0 + t;
+      if (row >= M) break;
+      float top = lds.m[0][t];
+#pragma unroll
+      for (int x = 1; x < kWaves; ++x) top = fmaxf(top, lds.m[x][t]);
+      float sum = 0.0f;
+      f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int x = 0; x < kWaves; ++x) {
+        const float f = exp2f(lds.m[x][t] - top);
+        sum += f * lds.l[x][t];
+        v += f * *(const f32x4*)&lds.o[x][t][d];
+      }
+      if (st.piece < 0) {
+        const int64_t at = row_at(row);
+        v *= sum == 0.0f ? 0.0f : 1.0f / sum;   // a row that sees nothing: 0
+        const bf16x2 lo = {(__bf16)v[0], (__bf16)v[1]}, hi = {(__bf16)v[2], (__bf16)v[3]};
+        *(u32x2*)(a.out + at * D + d) = u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+        if (d == 0) a.lse[at] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+      } else {
+        if (d == 0) *(f32x2*)piece_ml(a, st.piece, t) = f32x2{top, sum};
+        *(f32x4*)(piece_sums(a, st.piece, t) + d) = v;
+      }
     }
   }
 }
 
-// Joins the pieces of a split context: one workgroup per (query, head), its
-// threads side by side over the D values and, in kThreads * 4 / D groups, over
-// the pieces.
+// One workgroup, one item: its whole context.
+template <int D, int MT, int RG>
+__global__ void __launch_bounds__(kThreads, 2) kv8_attend_kernel(Kv8AttendArgs a) {
+  __shared__ AttendLds<D, MT, RG> lds;
+  const Kv8Cache& c = a.c;
+  // long row tiles first: a causal tile's work grows with its number
+  const int64_t tile = a.tiles - 1 - blockIdx.x / c.H;
+  int64_t base;
+  const int r = owner_of(a.cu, c.R, a.n_tok, a.G, 16 * MT * RG, 1, tile, base);
+  const Request q = request_at(a, r);
+  if ((tile - base) * 16 * MT * RG >= (int64_t)q.n * a.G) return;
+  attend_stretch<D, MT, RG>(a, q, Stretch{(int)(blockIdx.x % c.H), (int)(tile - base), 0, q.len, -1}, lds);
+}
+
+// Where the items are few and their contexts long, contexts are cut into
+// pieces of about the same length, whatever the requests' lengths: a.target of
+// them in all, enough to fill the chip once.  The host knows the lengths'
+// bound only, so the division is worked out here, by each wave for itself: 64
+// requests at a time, one to a lane.
+//   units_r  = 128-token units of an item of request r (at least one: an item
+//              that sees nothing has a result too)
+//   C        = ceil(sum over items of units / target), at least 4
+//   pieces_r = ceil(units_r / C), of ceil(units_r / pieces_r) units each
+// Piece numbers run over the requests, their items, and the pieces of each.
+constexpr int kUnit = kWaves * kStep;
+constexpr int kLeast = 4;
+struct Division {
+  Request q;
+  int items;          // of the request
+  int from;           // the first token its queries see, a multiple of 16
+  int units, pieces;  // of an item
+  int first;          // number of the request's first piece
+};
+__device__ __forceinline__ int items_of(const Kv8AttendArgs& a, const Request& q) {
+  return (int)(((int64_t)q.n * a.G + a.row_tile - 1) / a.row_tile) * a.c.H;
+}
+__device__ __forceinline__ int from_of(const Kv8AttendArgs& a, const Request& q) {
+  return min(seen_by(a, q, 0).lo, q.len) & ~15;
+}
+// The request that piece number `key` belongs to; false where there is none.
+__device__ __forceinline__ bool division_at(const Kv8AttendArgs& a, int key, Division& d) {
+  const int R = a.c.R, lane = threadIdx.x & 63;
+  Request q = {};
+  int items = 0, from = 0, units = 0, total = 0;
+  const auto look = [&](int r) {
+    items = 0;
+    if (r >= R) return;
+    q = request_at(a, r);
+    items = items_of(a, q);
+    from = from_of(a, q);
+    units = max(1, (q.len - from + kUnit - 1) / kUnit);
+  };
+  for (int r0 = 0; r0 < R; r0 += 64) {
+    look(r0 + lane);
+    total += items * units;
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) total += __shfl_xor(total, o);
+  const int C = max((total + a.target - 1) / a.target, kLeast);
+  int before = 0;
+  bool found = false;
+  for (int r0 = 0; r0 < R; r0 += 64) {
+    if (R > 64) look(r0 + lane);
+    const int pieces = (units + C - 1) / C, n = items > 0 ? items * pieces : 0;
+    int upto = n;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int y = __shfl_up(upto, o);
+      if (lane >= o) upto += y;
+    }
+    const int first = before + upto - n;
+    const bool under = r0 + lane < R && first <= key;
+    const uint64_t own = __ballot(under && n > 0), all = __ballot(under);
+    if (own) {
+      const int l = 63 - __clzll(own);
+      const auto at = [&](int x) { return __builtin_amdgcn_readlane(x, l); };
+      d.q = Request{at(q.r), at(q.n), (int64_t)at((int)q.c0), at(q.len), at(q.pos0)};
+      d.items = at(items);
+      d.from = at(from);
+      d.units = at(units);
+      d.pieces = at(pieces);
+      d.first = at(first);
+      found = true;
+    }
+    if (all != ~uint64_t(0)) break;
+    before = __builtin_amdgcn_readlane(before + upto, 63);
+  }
+  return found;
+}
+
+template <int D, int MT>
+__global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) kv8_attend_pieces_kernel(Kv8AttendArgs a) {
+  __shared__ AttendLds<D, MT, 1> lds;
+  Division d;
+  if (!division_at(a, blockIdx.x, d)) return;
+  const int in = (int)blockIdx.x - d.first, item = in / d.pieces, part = in - item * d.pieces;
+  if (item >= d.items) return;
+  const int per = (d.units + d.pieces - 1) / d.pieces * kUnit;
+  Stretch st;
+  st.tile = item / a.c.H;
+  st.h = item - st.tile * a.c.H;
+  st.from = d.from + part * per;
+  st.to = min(d.q.len, st.from + per);
+  st.piece = d.pieces == 1 ? -1 : (int64_t)blockIdx.x;
+  attend_stretch<D, MT, 1>(a, d.q, st, lds);
+}
+
+// Joins the pieces of the items that were cut: the workgroup of a piece takes
+// every pieces_r-th row of its item, its threads side by side over the D values
+// and, in kThreads * 4 / D groups, over the pieces.
 template <int D>
 __global__ void __launch_bounds__(kThreads) kv8_join_kernel(Kv8AttendArgs a) {
   constexpr int NG = kThreads * 4 / D;
   __shared__ float red_m[kWaves], red_l[NG];
   __shared__ f32x4 red_o[NG][D / 4];
-  const int64_t rows = a.n_tok * a.Hq, at = blockIdx.x;
-  const f32x2* ml = (const f32x2*)a.part + at;
-  const float* part = a.part + 2 * (int64_t)a.splits * rows;
-  float top = -3.402823466e38f;
-  for (int s = threadIdx.x; s < a.splits; s += kThreads) top = fmaxf(top, ml[s * rows][0]);
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-  if ((threadIdx.x & 63) == 0) red_m[threadIdx.x >> 6] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) top = fmaxf(top, red_m[w]);
+  Division x;
+  if (!division_at(a, blockIdx.x, x) || x.pieces == 1) return;
+  const int in = (int)blockIdx.x - x.first, item = in / x.pieces, part = in - item * x.pieces;
+  if (item >= x.items) return;
+  const int tile = item / a.c.H, h = item - tile * a.c.H;
+  const int64_t first = blockIdx.x - part;
+  const int rows = min(a.row_tile, x.q.n * a.G - tile * a.row_tile);
   const int d = threadIdx.x % (D / 4), grp = threadIdx.x / (D / 4);
-  float sum = 0.0f;
-  f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-  for (int s = grp; s < a.splits; s += NG) {
-    const f32x2 x = ml[s * rows];
-    if (x[1] == 0.0f) continue;      // nothing seen there: no sums were written
-    const float f = exp2f(x[0] - top);
-    sum += f * x[1];
-    v += f * *(const f32x4*)(part + (s * rows + at) * D + 4 * d);
-  }
-  red_o[grp][d] = v;
-  if (d == 0) red_l[grp] = sum;
-  __syncthreads();
-  if (grp != 0) return;
+  for (int row = part; row < rows; row += x.pieces) {
+    float top = -3.402823466e38f;
+    for (int s = threadIdx.x; s < x.pieces; s += kThreads) top = fmaxf(top, piece_ml(a, first + s, row)[0]);
 #pragma unroll
-  for (int i = 1; i < NG; ++i) {
-    sum += red_l[i];
-    v += red_o[i][d];
+    for (int o = 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+    if ((threadIdx.x & 63) == 0) red_m[threadIdx.x >> 6] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, red_m[w]);
+    float sum = 0.0f;
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+    for (int s = grp; s < x.pieces; s += NG) {
+      const f32x2 ml = *(const f32x2*)piece_ml(a, first + s, row);
+      const f32x4 y = *(const f32x4*)(piece_sums(a, first + s, row) + 4 * d);
+      const float f = exp2f(ml[0] - top);
+      sum = fmaf(f, ml[1], sum);
+      v += f * y;
+    }
+    red_o[grp][d] = v;
+    if (d == 0) red_l[grp] = sum;
+    __syncthreads();
+    if (grp == 0) {
+#pragma unroll
+      for (int i = 1; i < NG; ++i) {
+        sum += red_l[i];
+        v += red_o[i][d];
+      }
+      v *= sum == 0.0f ? 0.0f : 1.0f / sum;
+      const int full = tile * a.row_tile + row;
+      const int64_t at = (x.q.c0 + full / a.G) * a.Hq + h * a.G + full % a.G;
+      const bf16x2 lo = {(__bf16)v[0], (__bf16)v[1]}, hi = {(__bf16)v[2], (__bf16)v[3]};
+      *(u32x2*)(a.out + at * D + 4 * d) = u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+      if (d == 0) a.lse[at] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    }
+    __syncthreads();
   }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  const bf16x2 lo = {(__bf16)(v[0] * inv), (__bf16)(v[1] * inv)}, hi = {(__bf16)(v[2] * inv), (__bf16)(v[3] * inv)};
-  *(u32x2*)(a.out + at * D + 4 * d) = u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
-  if (d == 0) a.lse[at] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 // ---- accumulated weight ---------------------------------------------------
@@ -463,17 +755,23 @@ __global__ void __launch_bounds__(kThreads) kv8_weigh_kernel(Kv8AttendArgs a) {
 
 template <int D>
 hipError_t attend(const Kv8AttendArgs& a, hipStream_t stream) {
-  const bool two = a.n_tok * a.G > 16 * (int64_t)a.c.R;
-  const int64_t tiles = a.n_tok * a.G / (two ? 32 : 16) + a.c.R;
-  const int64_t grid = tiles * a.c.H * a.splits;
-  if (two)
-    kv8_attend_kernel<D, 2><<<dim3((unsigned)grid), kThreads, 0, stream>>>(a);
+  if (a.pieces == 0) {
+    const dim3 grid((unsigned)(a.tiles * a.c.H));
+    if (a.row_tile == 64)
+      kv8_attend_kernel<D, 2, 2><<<grid, kThreads, 0, stream>>>(a);
+    else if (a.row_tile == 32)
+      kv8_attend_kernel<D, 2, 1><<<grid, kThreads, 0, stream>>>(a);
+    else
+      kv8_attend_kernel<D, 1, 1><<<grid, kThreads, 0, stream>>>(a);
+    return hipGetLastError();
+  }
+  if (a.row_tile == 32)
+    kv8_attend_pieces_kernel<D, 2><<<dim3((unsigned)a.pieces), kThreads, 0, stream>>>(a);
   else
-    kv8_attend_kernel<D, 1><<<dim3((unsigned)grid), kThreads, 0, stream>>>(a);
+    kv8_attend_pieces_kernel<D, 1><<<dim3((unsigned)a.pieces), kThreads, 0, stream>>>(a);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.splits == 1) return e;
-  const int64_t rows = a.n_tok * a.Hq;
-  kv8_join_kernel<D><<<dim3((unsigned)rows), kThreads, 0, stream>>>(a);
+  if (e != hipSuccess) return e;
+  kv8_join_kernel<D><<<dim3((unsigned)a.pieces), kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -491,25 +789,33 @@ hipError_t weigh(const Kv8AttendArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-void kv8_attend_split(Kv8AttendArgs& a) {
-  const int TR = a.n_tok * a.G > 16 * (int64_t)a.c.R ? 32 : 16;
-  int64_t tiles = (a.n_tok * a.G + TR - 1) / TR;
-  if (tiles < a.c.R) tiles = a.c.R < a.n_tok ? a.c.R : a.n_tok;
-  int64_t span = a.c.max_len;   // tokens that one row tile looks at, at most
-  if (a.causal && a.window && (int64_t)a.window + TR + 16 < span) span = (int64_t)a.window + TR + 16;
-  const int64_t base = tiles * a.c.H;
-  int64_t splits = base > 0 ? 1536 / base : 1;
-  const int64_t most = span / 256;
-  if (splits > most) splits = most;
-  if (splits < 1) splits = 1;
-  const int64_t chunk = (span + splits - 1) / splits;
-  a.chunk = (int32_t)((chunk + kWaves * kStep - 1) / (kWaves * kStep) * (kWaves * kStep));
-  a.splits = (int32_t)((span + a.chunk - 1) / a.chunk);
-  if (a.splits < 1) a.splits = 1;
+void kv8_attend_plan(Kv8AttendArgs& a) {
+  const int64_t rows = a.n_tok * a.G, R = a.c.R;
+  a.row_tile = rows <= 16 * R ? 16 : 32;
+  int64_t tiles = (rows + a.row_tile - 1) / a.row_tile;
+  if (tiles < R) tiles = R < a.n_tok ? R : a.n_tok;
+  int64_t span = a.c.max_len;   // tokens that one request's queries see, at most
+  if (a.causal && a.window && a.window + a.n_tok + 16 < span) span = a.window + a.n_tok + 16;
+  // a workgroup for each item where the contexts are short or the items many
+  const int64_t items = tiles * a.c.H, units = (span + kUnit - 1) / kUnit;
+  int64_t most = rows / a.row_tile + R;        // items that there may be
+  if (most > rows) most = rows;
+  most *= a.c.H;
+  a.pieces = a.target = 0;
+  if (span > kLeast * kUnit && items < 1024 && most * units < 0x7fffffff) {
+    const int64_t fill = a.row_tile == 16 ? FILL : FILL * 2 / 3;
+    a.target = (int32_t)(items < fill ? fill - items / 2 : fill / 2);   // rounding up adds half a piece an item
+    // an item has at most one piece over its share, and none of fewer than kLeast units but the last
+    const int64_t each = (units + kLeast - 1) / kLeast;
+    a.pieces = (int32_t)(most * each < a.target + most ? most * each : a.target + most);
+  } else if (a.row_tile == 32 && rows > 48 * R) {
+    a.row_tile = 64;
+  }
+  a.tiles = rows / a.row_tile + R;
 }
 
 size_t kv8_attend_workspace(const Kv8AttendArgs& a) {
-  return a.splits == 1 ? 0 : (size_t)a.splits * a.n_tok * a.Hq * (2 + a.c.D) * sizeof(float);
+  return (size_t)a.pieces * a.row_tile * (2 + a.c.D) * sizeof(float);
 }
 
 hipError_t launch_kv8_attend(const Kv8AttendArgs& a, hipStream_t stream) {

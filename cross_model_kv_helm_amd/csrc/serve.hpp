@@ -70,14 +70,16 @@ struct Kv8AttendArgs {
   uint16_t* out;
   float* lse;                // written by attend, read by weigh
   float* weights;            // weigh
-  float* part;               // workspace of a split context: [splits][n_tok * Hq] (m, l), then [..][D] sums
+  float* part;               // workspace, where contexts are cut into pieces
   int64_t n_tok;
   int32_t Hq, G, causal, window;
   float scale_log2;          // softmax_scale * log2(e)
-  int32_t splits, chunk;     // pieces of the context and tokens in each
+  int32_t row_tile;          // rows of a workgroup
+  int32_t pieces, target;    // 0: a workgroup has an item's whole context; else workgroups launched, pieces aimed at
+  int64_t tiles;             // row tiles numbered, some of them empty; times H: items
 };
-// The pieces that a context is split into: a function of the shape alone.
-void kv8_attend_split(Kv8AttendArgs& a);
+// How attention is divided over workgroups: a function of the shape alone.
+void kv8_attend_plan(Kv8AttendArgs& a);
 size_t kv8_attend_workspace(const Kv8AttendArgs& a);
 hipError_t launch_kv8_attend(const Kv8AttendArgs& a, hipStream_t stream);
 hipError_t launch_kv8_weigh(const Kv8AttendArgs& a, hipStream_t stream);

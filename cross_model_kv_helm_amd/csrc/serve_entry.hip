@@ -126,7 +126,8 @@ int check_queries(const helm_kv8_shape_t* s) {
   if (s->causal != 0 && s->causal != 1) return fail(HELM_E_INVALID_ARG, "causal=%d must be 0 or 1", s->causal);
   if (s->window < 0 || (s->window > 0 && !s->causal))
     return fail(HELM_E_INVALID_ARG, "window=%d must be >= 0, and 0 without causal", s->window);
-  if (!std::isfinite(s->softmax_scale)) return fail(HELM_E_INVALID_ARG, "softmax_scale must be finite");
+  if (!std::isfinite(s->softmax_scale) || !(s->softmax_scale > 0.0))
+    return fail(HELM_E_INVALID_ARG, "softmax_scale must be finite and > 0 (%g)", s->softmax_scale);
   int64_t rows = s->n_tokens;
   if (!mul_ok(rows, s->n_q_heads) || rows > 0x7fffffffLL)
     return fail(HELM_E_INVALID_ARG, "n_tokens * n_q_heads exceeds 2^31-1");
@@ -160,7 +161,7 @@ helm::Kv8AttendArgs attend_args(const helm_kv8_shape_t* s) {
   // no request can hold more than its table's pages
   const int64_t room = (int64_t)s->max_blocks * s->block_size;
   if (room < a.c.max_len) a.c.max_len = (int32_t)room;
-  helm::kv8_attend_split(a);
+  helm::kv8_attend_plan(a);
   return a;
 }
 
@@ -341,6 +342,8 @@ int helm_kv8_attend(const void* q, const int32_t* cu, const int32_t* kv_len, con
       (rc = check_aligned(v_pool, "v_pool", 16)) || (rc = check_aligned(out, "out", 16)))
     return rc;
   helm::Kv8AttendArgs a = attend_args(s);
+  if (a.tiles * s->n_kv_heads > 0x7fffffffLL)
+    return fail(HELM_E_INVALID_ARG, "%lld row tiles of %d KV heads exceed 2^31-1", (long long)a.tiles, s->n_kv_heads);
   const size_t need = helm::kv8_attend_workspace(a);
   const int64_t rows = s->n_tokens * s->n_q_heads;
   Range outs[] = {{out, rows * D * 2, "out"}, {lse, rows * 4, "lse"}, {s->workspace, (int64_t)need, "workspace"}};

@@ -130,7 +130,8 @@ def test_shapes_refused(name, kw, status, text):
 @pytest.mark.parametrize("kw,status,text", [
     (dict(n_q_heads=12), 1, "multiple"), (dict(n_q_heads=0), 1, "multiple"), (dict(dtype=1), 5, "bf16"),
     (dict(causal=2), 1, "causal"), (dict(window=-1), 1, "window"), (dict(window=5, causal=0), 1, "window"),
-    (dict(softmax_scale=math.inf), 1, "softmax_scale"),
+    (dict(softmax_scale=math.inf), 1, "softmax_scale"), (dict(softmax_scale=0.0), 1, "softmax_scale"),
+    (dict(softmax_scale=-1.0), 1, "softmax_scale"),
     (dict(n_tokens=2 ** 31 - 1), 1, "n_tokens * n_q_heads")])
 def test_query_shapes_refused(name, kw, status, text):
     f, n = calls()[name]
