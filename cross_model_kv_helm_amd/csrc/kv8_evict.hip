@@ -3,14 +3,19 @@
 // Selection, one workgroup per (request, KV head): the weights become 32-bit
 // keys in the same order (NaN lowest), a radix selection of four 8-bit digits
 // finds the key of the last token that stays and how many equal ones stay with
-// it, and one ordered pass writes the kept indices ascending (the first of the
-// equal ones, so ties go to the lowest index).  Each pass reads the request's
-// weights again, from L2.
+// it, and each wave then writes the kept indices of its stretch of tokens,
+// ascending (the first of the equal ones, so ties go to the lowest index).
+// The keys are held in LDS where they fit (contexts up to 36,800 tokens), so
+// the weights are read once; else every pass reads them again.  Weights crowd
+// into few exponents: the histogram has 16 copies, one for every 16th lane, so
+// that at most four lanes meet in an atomic.
 //
-// Copy, one workgroup per (block written, head, K or V): the kept tokens'
-// codes, whose blocks have scales of their own, are taken to one new scale.
-// The blocks written are disjoint from the blocks read, so the copies need no
-// order.  Bound by memory: 2 bytes moved per kept value, 8 per token looked at.
+// Copy, one wave per (block written, head): the kept tokens' codes, whose
+// blocks have scales of their own, are taken to one new scale, K and V side by
+// side from one look at the indices and the table.  A block's codes stay in
+// registers between finding their size and writing them.  The blocks written
+// are disjoint from the blocks read, so the copies need no order.  Bound by
+// memory: 2 bytes moved per kept value, 8 per token looked at.
 #include "serve.hpp"
 
 namespace helm {
@@ -18,7 +23,10 @@ namespace {
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelWaves = kSelThreads / 64;
+constexpr int kCopies = 16;
 constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kKeysInLds = 36800;        // with the histogram just under 160 KB
 
 // Larger weight, larger key; -0 equals +0; NaN below -inf.
 __device__ __forceinline__ uint32_t key_of(float w) {
@@ -32,19 +40,26 @@ __device__ __forceinline__ int clamped_len(const Kv8Cache& c, int len) {
   return (int)max((int64_t)0, min(min((int64_t)len, (int64_t)c.max_len), room));
 }
 
-// Weight of token t of request r, head h; a token of an absent block: NaN (goes first).
-__device__ __forceinline__ float weight_at(const Kv8EvictArgs& a, const int32_t* row, int h, int t) {
-  const Kv8Cache& c = a.c;
-  const int page = c.page_magic ? (int)__umulhi((uint32_t)t >> 4, c.page_magic) : t >> 4;
-  const int blk = row[page];
-  if ((uint32_t)blk >= (uint32_t)c.n_blocks) return __builtin_nanf("");
-  return a.weights[((int64_t)blk * c.H + h) * c.B + (t - page * c.B)];
+__device__ __forceinline__ int page_of(const Kv8Cache& c, int t) {
+  return c.page_magic ? (int)__umulhi((uint32_t)t >> 4, c.page_magic) : t >> 4;
 }
 
+// Keys of tokens t .. t+3 (t a multiple of 4: all of one block); a token of an
+// absent block has the lowest (goes first).
+__device__ __forceinline__ u32x4 keys_at(const Kv8EvictArgs& a, const int32_t* row, int h, int t) {
+  const Kv8Cache& c = a.c;
+  const int page = page_of(c, t), blk = row[page];
+  if ((uint32_t)blk >= (uint32_t)c.n_blocks) return u32x4{0, 0, 0, 0};
+  const float* w = a.weights + ((int64_t)blk * c.H + h) * c.B + (t - page * c.B);
+  return u32x4{key_of(w[0]), key_of(w[1]), key_of(w[2]), key_of(w[3])};
+}
+
+template <bool LDS>
 __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(Kv8EvictArgs a) {
-  __shared__ int hist[256];
+  extern __shared__ uint32_t keys[];
+  __shared__ int hist[256 * kCopies];
   __shared__ int found[2];                 // digit, how many of the tokens above stay
-  __shared__ int above[2][kSelWaves], equal[2][kSelWaves];
+  __shared__ int above[kSelWaves], equal[kSelWaves];
   const Kv8Cache& c = a.c;
   const int r = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int n = clamped_len(c, a.kv_len[r]);
@@ -60,18 +75,35 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(Kv8EvictArgs a)
   const int cand = n - a.recent;           // tokens that compete
   int need = a.budget - a.recent;          // how many of them stay: 0 <= need < cand
 
+  if constexpr (LDS) {
+#pragma unroll 4
+    for (int t = 4 * tid; t < cand; t += 4 * kSelThreads) *(u32x4*)&keys[t] = keys_at(a, row, h, t);
+    __syncthreads();
+  }
+  const auto four = [&](int t) { return LDS ? *(const u32x4*)&keys[t] : keys_at(a, row, h, t); };
+
   uint32_t prefix = 0, mask = 0;           // the digits found so far
   for (int shift = 24; need > 0 && shift >= 0; shift -= 8) {
-    for (int j = tid; j < 256; j += kSelThreads) hist[j] = 0;
+    for (int j = tid; j < 256 * kCopies; j += kSelThreads) hist[j] = 0;
     __syncthreads();
-    for (int t = tid; t < cand; t += kSelThreads) {
-      const uint32_t k = key_of(weight_at(a, row, h, t));
-      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
+    for (int t = 4 * tid; t < cand; t += 4 * kSelThreads) {
+      const u32x4 k = four(t);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (t + i < cand && (k[i] & mask) == prefix)
+          atomicAdd(&hist[((k[i] >> shift) & 255) * kCopies + (lane & (kCopies - 1))], 1);
+    }
+    __syncthreads();
+    if (tid < 256) {
+      int sum = 0;
+#pragma unroll
+      for (int j = 0; j < kCopies; ++j) sum += hist[tid * kCopies + ((j + tid) & (kCopies - 1))];
+      hist[tid * kCopies] = sum;           // a thread reads and writes its own digit's copies only
     }
     __syncthreads();
     if (wave == 0) {   // from the largest digit down: lane l looks at digits 255-4l .. 252-4l
       int own = 0;
-      for (int j = 0; j < 4; ++j) own += hist[255 - 4 * lane - j];
+      for (int j = 0; j < 4; ++j) own += hist[(255 - 4 * lane - j) * kCopies];
       int before = own;
       for (int o = 1; o < 64; o <<= 1) {
         const int x = __shfl_up(before, o);
@@ -80,7 +112,7 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(Kv8EvictArgs a)
       before -= own;
       if (before < need && before + own >= need) {
         int d = 255 - 4 * lane;
-        while (before + hist[d] < need) before += hist[d--];
+        while (before + hist[d * kCopies] < need) before += hist[d-- * kCopies];
         found[0] = d;
         found[1] = before;
       }
@@ -93,39 +125,78 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(Kv8EvictArgs a)
   }
   // need: how many tokens of key `prefix` stay (0 only where none competes)
 
-  int written = 0, same = 0;               // kept so far, equal ones seen so far
-  for (int t0 = 0, buf = 0; t0 < n; t0 += kSelThreads, buf ^= 1) {
-    const int t = t0 + tid;
-    const uint32_t k = t < cand ? key_of(weight_at(a, row, h, t)) : 0u;
-    const bool over = t < n && (t >= cand || (need > 0 && k > prefix));
-    const bool tie = t < cand && need > 0 && k == prefix;
-    const uint64_t bo = __ballot(over), be = __ballot(tie);
-    if (lane == 0) {
-      above[buf][wave] = __popcll(bo);
-      equal[buf][wave] = __popcll(be);
+  // each wave's stretch of the tokens: first what it holds, then where it goes
+  const int per = (n + kSelThreads * 4 - 1) / (kSelThreads * 4) * 256;
+  const int t0 = min(wave * per, n), t1 = min(t0 + per, n);
+  const auto kind = [&](int t, u32x4 k, int i) {       // 2: above, 1: equal, 0: neither
+    if (t + i >= t1) return 0;
+    if (t + i >= cand) return 2;
+    return need > 0 ? (k[i] > prefix ? 2 : k[i] == prefix ? 1 : 0) : 0;
+  };
+  int over = 0, ties = 0;
+  for (int t = t0 + 4 * lane; t < t1; t += 256) {
+    const u32x4 k = t < cand ? four(t) : u32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int x = kind(t, k, i);
+      over += x == 2;
+      ties += x == 1;
     }
-    __syncthreads();
-    int o_before = 0, e_before = 0, o_all = 0, e_all = 0;
-    for (int w = 0; w < kSelWaves; ++w) {
-      const int o = above[buf][w], e = equal[buf][w];
-      if (w < wave) { o_before += o; e_before += e; }
-      o_all += o;
-      e_all += e;
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) {
+    over += __shfl_xor(over, o);
+    ties += __shfl_xor(ties, o);
+  }
+  if (lane == 0) {
+    above[wave] = over;
+    equal[wave] = ties;
+  }
+  __syncthreads();
+  int written = 0, same = 0;               // kept before this point by rank, equal ones seen
+  for (int w = 0; w < wave; ++w) {
+    written += above[w];
+    same += equal[w];
+  }
+  written += min(same, need);
+  for (int t = t0; t < t1; t += 256) {     // all lanes stay in the loop: they exchange counts
+    const int mine = t + 4 * lane;
+    const u32x4 k = mine < cand ? four(mine) : u32x4{0, 0, 0, 0};
+    int x[4], o = 0, e = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = kind(mine, k, i);
+      o += x[i] == 2;
+      e += x[i] == 1;
     }
-    const uint64_t low = (uint64_t(1) << lane) - 1;
-    const int e_rank = same + e_before + __popcll(be & low);       // equal tokens before this one
-    const int at = written + o_before + __popcll(bo & low) + (min(e_rank, need) - min(same, need));
-    if (over || (tie && e_rank < need)) kept[at] = t;
-    written += o_all + (min(same + e_all, need) - min(same, need));
-    same += e_all;
+    int both = o << 16 | e, upto = both;   // at most 256 of each
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+      const int y = __shfl_up(upto, s);
+      if (lane >= s) upto += y;
+    }
+    const int all = __builtin_amdgcn_readlane(upto, 63);
+    upto -= both;
+    int at_o = upto >> 16, at_e = same + (upto & 0xffff);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (x[i] == 2 || (x[i] == 1 && at_e < need))
+        kept[written + at_o + (min(at_e, need) - min(same, need))] = mine + i;
+      at_o += x[i] == 2;
+      at_e += x[i] == 1;
+    }
+    written += (all >> 16) + (min(same + (all & 0xffff), need) - min(same, need));
+    same += all & 0xffff;
   }
 }
 
+// U 16-byte pieces of K and of V a lane at a time: a whole block where it has
+// no more (WHOLE), else the codes are read again to be written.
+template <int U, bool WHOLE>
 __global__ void __launch_bounds__(kThreads) kv8_copy_kernel(Kv8EvictArgs a) {
-  __shared__ float red[kThreads / 64];
   const Kv8Cache& c = a.c;
-  const int page = blockIdx.x, h = blockIdx.y, r = blockIdx.z >> 1;
-  const bool is_v = blockIdx.z & 1;
+  const int lane = threadIdx.x & 63;
+  const int page = blockIdx.x * kWaves + (threadIdx.x >> 6), h = blockIdx.y, r = blockIdx.z;
   const int keep = min(clamped_len(c, a.kv_len[r]), a.budget);
   const int j0 = page * c.B;
   if (j0 >= keep) return;
@@ -134,70 +205,129 @@ __global__ void __launch_bounds__(kThreads) kv8_copy_kernel(Kv8EvictArgs a) {
   const int cnt = min(c.B, keep - j0);
   const int32_t* kept = a.kept + ((int64_t)r * c.H + h) * a.budget + j0;
   const int32_t* row = c.table + (int64_t)r * c.max_blocks;
-  const uint8_t* pool = is_v ? c.v_pool : c.k_pool;
-  const float* scales = is_v ? c.v_scale : c.k_scale;
   const int per = c.D / 16, shift = 31 - __clz(per);   // 16-byte pieces of a token
-
+  const int all = c.B * per;
   const int64_t dst = (int64_t)blk * c.H + h;
-  float amax = 0.0f;
-  // first the size of what is kept, then (from the caches) its codes
-  for (int phase = 0; phase < 2; ++phase) {
-    float inv = 0.0f;
-    if (phase) {
+
+  u32x4 k[U], v[U];
+  float ks[U], vs[U], wt[U], k_max = 0.0f, v_max = 0.0f;
+  const auto load = [&](int u0) {
+    int64_t from[U];
+    int off[U];
 #pragma unroll
-      for (int o = 32; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
-      if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = amax;
-      __syncthreads();
-#pragma unroll
-      for (int w = 0; w < kThreads / 64; ++w) amax = fmaxf(amax, red[w]);
-      const float now = kv8_scale_of(amax);
-      inv = 1.0f / now;
-      if (threadIdx.x == 0) (is_v ? c.v_scale : c.k_scale)[dst] = now;
+    for (int i = 0; i < U; ++i) {
+      const int u = u0 + i * 64 + lane, j = u >> shift;
+      from[i] = -1;
+      off[i] = 0;
+      if (u < all && j < cnt) {
+        const int t = kept[j], sp = page_of(c, t), sb = row[sp];
+        off[i] = t - sp * c.B;
+        if ((uint32_t)sb < (uint32_t)c.n_blocks) from[i] = (int64_t)sb * c.H + h;
+      }
     }
-    for (int u = threadIdx.x; u < c.B * per; u += kThreads) {
-      const int j = u >> shift, part = u & (per - 1);
-      u32x4 w = {0, 0, 0, 0};
-      float s = 0.0f;
-      if (j < cnt) {
-        const int t = kept[j];
-        const int sp = c.page_magic ? (int)__umulhi((uint32_t)t >> 4, c.page_magic) : t >> 4;
-        const int sb = row[sp];
-        if ((uint32_t)sb < (uint32_t)c.n_blocks) {
-          const int64_t from = (int64_t)sb * c.H + h;
-          s = scales[from];
-          w = *(const u32x4*)(pool + (from * c.B + (t - sp * c.B)) * c.D + part * 16);
-          if (phase && !is_v && part == 0) a.weights[dst * c.B + j] = a.weights[from * c.B + (t - sp * c.B)];
-        } else if (phase && !is_v && part == 0) {
-          a.weights[dst * c.B + j] = 0.0f;
-        }
-      } else if (phase && !is_v && part == 0) {
-        a.weights[dst * c.B + j] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int part = lane & (per - 1);               // 64 is a multiple of a token's pieces
+      k[i] = v[i] = u32x4{0, 0, 0, 0};
+      ks[i] = vs[i] = wt[i] = 0.0f;
+      if (from[i] >= 0) {
+        const int64_t slot = from[i] * c.B + off[i];
+        k[i] = *(const u32x4*)(c.k_pool + slot * c.D + part * 16);
+        v[i] = *(const u32x4*)(c.v_pool + slot * c.D + part * 16);
+        ks[i] = c.k_scale[from[i]];
+        vs[i] = c.v_scale[from[i]];
+        if (part == 0) wt[i] = a.weights[slot];
       }
+    }
+  };
+  const auto size = [&]() {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f32x4 x = kv8_decode4(w[i]);
-        if (!phase) {
+    for (int i = 0; i < U; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) amax = fmaxf(amax, kv8_size(x[e] * s));
-        } else {
-          const float f = s * inv;
-          w[i] = kv8_encode4(x[0] * f, x[1] * f, x[2] * f, x[3] * f);
+      for (int e = 0; e < 4; ++e) {
+        const f32x4 x = kv8_decode4(k[i][e]), y = kv8_decode4(v[i][e]);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          k_max = fmaxf(k_max, kv8_size(x[b] * ks[i]));
+          v_max = fmaxf(v_max, kv8_size(y[b] * vs[i]));
         }
       }
-      if (phase) *(u32x4*)((is_v ? c.v_pool : c.k_pool) + (dst * c.B + j) * c.D + part * 16) = w;
+  };
+  if constexpr (WHOLE) {
+    load(0);
+    size();
+  } else {
+    for (int u0 = 0; u0 < all; u0 += 64 * U) {
+      load(u0);
+      size();
     }
   }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) {
+    k_max = fmaxf(k_max, __shfl_xor(k_max, o));
+    v_max = fmaxf(v_max, __shfl_xor(v_max, o));
+  }
+  const float k_now = kv8_scale_of(k_max), v_now = kv8_scale_of(v_max);
+  const float k_inv = 1.0f / k_now, v_inv = 1.0f / v_now;
+  if (lane == 0) {
+    c.k_scale[dst] = k_now;
+    c.v_scale[dst] = v_now;
+  }
+  for (int u0 = 0; u0 < all; u0 += 64 * U) {
+    if constexpr (!WHOLE) load(u0);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int u = u0 + i * 64 + lane;
+      if (u >= all) break;
+      const float kf = ks[i] * k_inv, vf = vs[i] * v_inv;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const f32x4 x = kv8_decode4(k[i][e]), y = kv8_decode4(v[i][e]);
+        k[i][e] = kv8_encode4(x[0] * kf, x[1] * kf, x[2] * kf, x[3] * kf);
+        v[i][e] = kv8_encode4(y[0] * vf, y[1] * vf, y[2] * vf, y[3] * vf);
+      }
+      *(u32x4*)(c.k_pool + dst * c.B * c.D + (int64_t)u * 16) = k[i];
+      *(u32x4*)(c.v_pool + dst * c.B * c.D + (int64_t)u * 16) = v[i];
+      if ((lane & (per - 1)) == 0) a.weights[dst * c.B + (u >> shift)] = wt[i];
+    }
+    if constexpr (WHOLE) break;
+  }
+}
+
+template <int U>
+void copy(const Kv8EvictArgs& a, hipStream_t stream) {
+  const Kv8Cache& c = a.c;
+  const int pages = (a.budget + c.B - 1) / c.B;
+  const dim3 grid((unsigned)((pages + kWaves - 1) / kWaves), (unsigned)c.H, (unsigned)c.R);
+  if (c.B * (c.D / 16) <= 64 * U)
+    kv8_copy_kernel<U, true><<<grid, kThreads, 0, stream>>>(a);
+  else
+    kv8_copy_kernel<U, false><<<grid, kThreads, 0, stream>>>(a);
 }
 
 }  // namespace
 
 hipError_t launch_kv8_evict(const Kv8EvictArgs& a, hipStream_t stream) {
   const Kv8Cache& c = a.c;
-  kv8_select_kernel<<<dim3((unsigned)c.R, (unsigned)c.H), kSelThreads, 0, stream>>>(a);
-  hipError_t e = hipGetLastError();
+  const dim3 grid((unsigned)c.R, (unsigned)c.H);
+  const int64_t room = (int64_t)c.max_blocks * c.B, longest = room < c.max_len ? room : c.max_len;
+  if (longest <= kKeysInLds) {
+    const size_t lds = (size_t)(longest + 3) / 4 * 16;
+    if (lds > (32u << 10)) {   // with the histogram near the default bound of 64 KB or over it
+      const hipError_t e = hipFuncSetAttribute((const void*)kv8_select_kernel<true>,
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, kKeysInLds * 4);
+      if (e != hipSuccess) return e;
+    }
+    kv8_select_kernel<true><<<grid, kSelThreads, lds, stream>>>(a);
+  } else {
+    kv8_select_kernel<false><<<grid, kSelThreads, 0, stream>>>(a);
+  }
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const dim3 grid((unsigned)((a.budget + c.B - 1) / c.B), (unsigned)c.H, (unsigned)c.R * 2);
-  kv8_copy_kernel<<<grid, kThreads, 0, stream>>>(a);
+  if (c.B * (c.D / 16) <= 128)
+    copy<2>(a, stream);
+  else
+    copy<4>(a, stream);
   return hipGetLastError();
 }
 
