@@ -32,6 +32,12 @@
 namespace helm {
 namespace {
 
+#ifndef WA
+#define WA 2
+#endif
+#ifndef WFILL
+#define WFILL 768
+#endif
 #ifndef FILL
 #define FILL 768
 #endif
@@ -114,11 +120,16 @@ __device__ __forceinline__ void load_k(const Kv8Cache& c, const Tile& x, int g, 
   for (int i = 0; i < D / 64; ++i) w[i] = *(const u32x4*)(p + lane + 16 * i);
 }
 
+// Query of a row: row / G as a 64-bit product, see group_magic_of.
+__device__ __forceinline__ int query_of(const Kv8AttendArgs& a, int row) {
+  return (int)((uint64_t)(uint32_t)row * a.g_magic >> a.g_shift);
+}
+
 // 16 queries as the right operand of S^T: this lane's row, d = g*D/4 + 8s.
 template <int D>
 __device__ __forceinline__ void load_q(const Kv8AttendArgs& a, const Request& q, int h, int row, int g,
                                        bf16x8 (&v)[D / 32]) {
-  const int i = row / a.G;
+  const int i = query_of(a, row);
   const uint16_t* p = a.q + (q.c0 + i) * a.q_tok + (int64_t)(h * a.G + row - i * a.G) * a.q_head + g * (D / 4);
 #pragma unroll
   for (int s = 0; s < D / 32; ++s) __builtin_memcpy(&v[s], p + 8 * s, 16);
@@ -298,7 +309,7 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
     const int row = min(rowg + 16 * t + m, M - 1);
-    see[t] = seen_by(a, q, row / a.G);
+    see[t] = seen_by(a, q, query_of(a, row));
     load_q<D>(a, q, h, row, g, qv[t]);
   }
   const int last = min(rowg + 16 * MT, M) - 1;
@@ -431,7 +442,7 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
     l[t] += __shfl_xor(l[t], 32);
   }
   const auto row_at = [&](int row) {
-    const int i = row / a.G;
+    const int i = query_of(a, row);
     return (q.c0 + i) * a.Hq + h * a.G + (row - i * a.G);
   };
   const auto put = [&](int t, int slot) {     // this wave's row tile t for the others
@@ -676,80 +687,223 @@ __global__ void __launch_bounds__(kThreads) kv8_join_kernel(Kv8AttendArgs a) {
 }
 
 // ---- accumulated weight ---------------------------------------------------
-// The scores again, with 2^(x - lse) summed over the rows.  Each weight is
-// summed by one workgroup.  ROWS: the waves share 64 tokens and take row tiles
-// in turn (prompts); else each wave has 32 tokens of its own (few rows).
-template <int D, bool ROWS>
-__global__ void __launch_bounds__(kThreads) kv8_weigh_kernel(Kv8AttendArgs a) {
-  constexpr int SUB = ROWS ? 4 : 2;
-  __shared__ float red[ROWS ? kWaves : 1][64];
+// The scores again, this time S = Q K^T with 2^(x - lse) summed over the rows:
+// a lane holds four rows of one token, so the sum over a row tile stays in the
+// lane but for one exchange among its four groups at the end.  Each weight is
+// summed by one workgroup, in a fixed order.
+template <int D>
+struct RowTile {     // 16 rows, as loaded: this lane's operand and lse are row m's
+  bf16x8 q[D / 32];
+  float lse;
+};
+template <int D>
+__device__ __forceinline__ void load_rows(const Kv8AttendArgs& a, const Request& q, int h, int row0, int g, int m,
+                                          RowTile<D>& x) {
+  const int row = min(row0 + m, q.n * a.G - 1), i = query_of(a, row), head = h * a.G + row - i * a.G;
+  const uint16_t* p = a.q + (q.c0 + i) * a.q_tok + head * a.q_head + g * (D / 4);
+#pragma unroll
+  for (int s = 0; s < D / 32; ++s) __builtin_memcpy(&x.q[s], p + 8 * s, 16);
+  x.lse = a.lse[(q.c0 + i) * a.Hq + head];
+}
+// lse of rows 4g..4g+3 in units of log2; a row past the end, or whose lse is
+// not finite, adds nothing.
+__device__ __forceinline__ void row_lse(float lse, bool row_exists, int g, float (&z)[4]) {
+  lse = row_exists && fabsf(lse) <= 3.402823466e38f ? lse * kLog2e : INFINITY;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) z[i] = __shfl(lse, 4 * g + i);
+}
+
+// Adds to acc what 16 rows give tokens tok, tok + 16, ...: the products of all
+// SUB tiles first, so that none waits for its own chain.
+template <int D, int SUB>
+__device__ __forceinline__ void add_weights(const Kv8AttendArgs& a, const Request& r, const bf16x8 (&q)[D / 32],
+                                            const bf16x8 (&k)[SUB][D / 32], const float (&ks)[SUB],
+                                            const float (&lse)[4], int row, bool all, int tok, float (&acc)[SUB]) {
+  f32x4 s[SUB];
+#pragma unroll
+  for (int u = 0; u < SUB; ++u) s[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+    for (int u = 0; u < SUB; ++u) s[u] = mfma(q[i], k[u][i], s[u]);
+  if (all) {
+#pragma unroll
+    for (int u = 0; u < SUB; ++u) {
+      float p[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[i] = __builtin_amdgcn_exp2f(fmaf(s[u][i], ks[u], -lse[i]));
+      acc[u] += (p[0] + p[1]) + (p[2] + p[3]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const Seen see = seen_by(a, r, query_of(a, row + i));      // a row past the end adds 0 anyway
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) {
+        const float p = __builtin_amdgcn_exp2f(fmaf(s[u][i], ks[u], -lse[i]));
+        acc[u] += tok + 16 * u < see.lo || tok + 16 * u >= see.hi ? 0.0f : p;
+      }
+    }
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void convert_k(const u32x4 (&w)[D / 64], bf16x8 (&k)[D / 32]) {
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    k[2 * i] = cvt8(w[i][0], w[i][1]);
+    k[2 * i + 1] = cvt8(w[i][2], w[i][3]);
+  }
+}
+
+// Few rows: a wave streams through its stretch of the context, 32 tokens at a
+// time with the next keys in flight, the first row tile in registers.
+template <int D>
+__device__ __forceinline__ void weigh_stretch(const Kv8AttendArgs& a, const Request& q, int h, int from, int to) {
+  const Kv8Cache& c = a.c;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
+  const int M = q.n * a.G;
+  const int32_t* table = c.table + (int64_t)q.r * c.max_blocks;
+  RowTile<D> rows;
+  float lse[4];
+  load_rows<D>(a, q, h, 0, g, m, rows);
+  row_lse(rows.lse, m < M, g, lse);
+  const Seen s_first = seen_by(a, q, 0), s_last = seen_by(a, q, query_of(a, min(16, M) - 1));
+  const auto tiles = [&](int t, Tile (&x)[2]) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) x[u] = tile_at(c, table, h, t + 16 * u, to);
+  };
+  int t0 = from + wave * kStep;
+  Tile now[2], next[2];
+  u32x4 kw[2][D / 64];
+  float ks[2];
+  tiles(t0, now);
+  tiles(t0 + kUnit, next);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    load_k<D>(c, now[u], g, m, kw[u]);
+    ks[u] = c.k_scale[now[u].slab];
+  }
+  for (; t0 < to; t0 += kUnit) {
+    bf16x8 k[2][D / 32];
+    float scale[2], was = 0.0f;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      convert_k<D>(kw[u], k[u]);
+      scale[u] = ks[u] * a.scale_log2;
+      load_k<D>(c, next[u], g, m, kw[u]);
+      ks[u] = c.k_scale[next[u].slab];
+    }
+    Tile after[2];
+    tiles(t0 + 2 * kUnit, after);
+    const int tok = t0 + lane;                  // of the 32, by lanes 0..31
+    const Tile& mine = g == 1 ? now[1] : now[0];
+    float* w = a.weights + mine.slab * c.B + mine.off + m;
+    const bool own = g < 2 && mine.ok && tok < to;
+    if (own) was = *w;
+    float acc[2] = {0.0f, 0.0f};
+    add_weights<D, 2>(a, q, rows.q, k, scale, lse, 4 * g, t0 >= s_last.lo && t0 + kStep <= s_first.hi, t0 + m, acc);
+    for (int row0 = 16; row0 < M; row0 += 16) {
+      RowTile<D> x;
+      float z[4];
+      load_rows<D>(a, q, h, row0, g, m, x);
+      row_lse(x.lse, row0 + m < M, g, z);
+      add_weights<D, 2>(a, q, x.q, k, scale, z, row0 + 4 * g, false, t0 + m, acc);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      acc[u] += __shfl_xor(acc[u], 16);
+      acc[u] += __shfl_xor(acc[u], 32);
+    }
+    if (own) *w = was + (g == 0 ? acc[0] : acc[1]);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      now[u] = next[u];
+      next[u] = after[u];
+    }
+  }
+}
+
+// One workgroup, one request and KV head.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 3) kv8_weigh_kernel(Kv8AttendArgs a) {
+  const Request q = request_at(a, blockIdx.x / a.c.H);
+  if (q.n > 0) weigh_stretch<D>(a, q, blockIdx.x % a.c.H, from_of(a, q), q.len);
+}
+// One workgroup, one piece of the division (whose items have all rows).
+template <int D>
+__global__ void __launch_bounds__(kThreads, 3) kv8_weigh_pieces_kernel(Kv8AttendArgs a) {
+  Division d;
+  if (!division_at(a, blockIdx.x, d)) return;
+  const int in = (int)blockIdx.x - d.first, item = in / d.pieces, part = in - item * d.pieces;
+  if (item >= d.items) return;
+  const int per = (d.units + d.pieces - 1) / d.pieces * kUnit, from = d.from + part * per;
+  weigh_stretch<D>(a, d.q, item, from, min(d.q.len, from + per));
+}
+
+// Many rows (prompts): the waves share 64 tokens, whose keys stay in registers,
+// and take row tiles in turn, the queries of the next ones in flight.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2) kv8_weigh_rows_kernel(Kv8AttendArgs a) {
+  constexpr int SUB = 4, AHEAD = WA;     // row tiles in flight
+  __shared__ float red[kWaves][16 * SUB];
   const Kv8Cache& c = a.c;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
   const int h = blockIdx.y;
   const Request q = request_at(a, blockIdx.z);
-  const int t0 = blockIdx.x * (ROWS ? 64 : 128) + (ROWS ? 0 : wave * 32);
-  if (blockIdx.x * (ROWS ? 64 : 128) >= q.len) return;
-
+  const int t0 = blockIdx.x * 16 * SUB;
+  if (t0 >= q.len) return;
   const int32_t* table = c.table + (int64_t)q.r * c.max_blocks;
   Tile x[SUB];
-  u32x4 kw[SUB][D / 64];
-  float ks[SUB];
-  f32x4 acc[SUB];
+  bf16x8 k[SUB][D / 32];
+  float ks[SUB], acc[SUB];
 #pragma unroll
   for (int u = 0; u < SUB; ++u) {
+    u32x4 kw[D / 64];
     x[u] = tile_at(c, table, h, t0 + 16 * u, q.len);
-    load_k<D>(c, x[u], g, m, kw[u]);
+    load_k<D>(c, x[u], g, m, kw);
     ks[u] = c.k_scale[x[u].slab] * a.scale_log2;
-    acc[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    convert_k<D>(kw, k[u]);
+    acc[u] = 0.0f;
   }
   const int M = q.n * a.G;
-  for (int row0 = ROWS ? 16 * wave : 0; row0 < M; row0 += ROWS ? 16 * kWaves : 16) {
-    const Seen s_first = seen_by(a, q, row0 / a.G), s_last = seen_by(a, q, (min(row0 + 16, M) - 1) / a.G);
-    if (s_last.hi <= t0 || s_first.lo >= t0 + 16 * SUB) continue;
-    const int row = min(row0 + m, M - 1), i = row / a.G;
-    bf16x8 qv[D / 32];
-    load_q<D>(a, q, h, row, g, qv);
-    const Seen see = seen_by(a, q, i);
-    float lse = a.lse[(q.c0 + i) * a.Hq + h * a.G + (row - i * a.G)] * kLog2e;
-    if (row0 + m >= M || !(fabsf(lse) <= 3.402823466e38f)) lse = INFINITY;   // adds nothing
+  // causal: the rows that see these tokens begin with those of query t0 - pos0
+  int row0 = 16 * wave;
+  if (a.causal && t0 > q.pos0) row0 += (int)min((int64_t)(t0 - q.pos0) * a.G / (16 * kWaves) * (16 * kWaves), (int64_t)M);
+  RowTile<D> rows[AHEAD];
 #pragma unroll
-    for (int u = 0; u < SUB; ++u) {
-      const f32x4 s = scores<D>(kw[u], qv);
+  for (int b = 0; b < AHEAD - 1; ++b)
+    if (M > 0) load_rows<D>(a, q, h, row0 + b * 16 * kWaves, g, m, rows[b]);
+  for (; row0 < M; row0 += AHEAD * 16 * kWaves) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int tok = t0 + 16 * u + 4 * g + e;
-        const float p = __builtin_amdgcn_exp2f(fmaf(s[e], ks[u], -lse));
-        acc[u][e] += x[u].ok && tok >= see.lo && tok < see.hi ? p : 0.0f;
-      }
+    for (int b = 0; b < AHEAD; ++b) {
+      const int row = row0 + b * 16 * kWaves;
+      if (row >= M) break;
+      load_rows<D>(a, q, h, row + (AHEAD - 1) * 16 * kWaves, g, m, rows[(b + AHEAD - 1) % AHEAD]);
+      const Seen s_first = seen_by(a, q, query_of(a, row)), s_last = seen_by(a, q, query_of(a, min(row + 16, M) - 1));
+      if (s_last.hi <= t0 || s_first.lo >= t0 + 16 * SUB) continue;
+      const bool all = s_last.lo <= t0 && s_first.hi >= t0 + 16 * SUB;
+      float lse[4];
+      row_lse(rows[b].lse, row + m < M, g, lse);
+      add_weights<D, SUB>(a, q, rows[b].q, k, ks, lse, row + 4 * g, all, t0 + m, acc);
     }
   }
 #pragma unroll
   for (int u = 0; u < SUB; ++u) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-#pragma unroll
-      for (int o = 1; o < 16; o <<= 1) acc[u][e] += __shfl_xor(acc[u][e], o);
-    }
-    if constexpr (ROWS) {
-      if (m == 0) *(f32x4*)&red[wave][16 * u + 4 * g] = acc[u];
-    } else if (m == 0 && x[u].ok) {
-      float* w = a.weights + x[u].slab * c.B + x[u].off + 4 * g;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (t0 + 16 * u + 4 * g + e < q.len) w[e] += acc[u][e];
-    }
+    acc[u] += __shfl_xor(acc[u], 16);
+    acc[u] += __shfl_xor(acc[u], 32);
+    if (g == u) red[wave][lane] = acc[u];
   }
-  if constexpr (ROWS) {
-    __syncthreads();
-    if (wave == 0) {
-      float sum = red[0][lane];
+  __syncthreads();
+  if (wave == 0) {
+    float sum = red[0][lane];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) sum += red[w][lane];
+    for (int w = 1; w < kWaves; ++w) sum += red[w][lane];
 #pragma unroll
-      for (int u = 0; u < SUB; ++u)
-        if (g == u && x[u].ok && t0 + lane < q.len) a.weights[x[u].slab * c.B + x[u].off + m] += sum;
-    }
+    for (int u = 0; u < SUB; ++u)
+      if (g == u && x[u].ok && t0 + lane < q.len) a.weights[x[u].slab * c.B + x[u].off + m] += sum;
   }
 }
 
@@ -777,41 +931,48 @@ hipError_t attend(const Kv8AttendArgs& a, hipStream_t stream) {
 
 template <int D>
 hipError_t weigh(const Kv8AttendArgs& a, hipStream_t stream) {
-  const bool rows = a.n_tok * a.G > 32 * (int64_t)a.c.R;
-  const int per = rows ? 64 : 128;
-  const dim3 grid((unsigned)((a.c.max_len + per - 1) / per), (unsigned)a.c.H, (unsigned)a.c.R);
-  if (rows)
-    kv8_weigh_kernel<D, true><<<grid, kThreads, 0, stream>>>(a);
-  else
-    kv8_weigh_kernel<D, false><<<grid, kThreads, 0, stream>>>(a);
+  if (a.n_tok * a.G > 64 * (int64_t)a.c.R) {
+    const dim3 grid((unsigned)((a.c.max_len + 63) / 64), (unsigned)a.c.H, (unsigned)a.c.R);
+    kv8_weigh_rows_kernel<D><<<grid, kThreads, 0, stream>>>(a);
+  } else if (a.pieces) {
+    kv8_weigh_pieces_kernel<D><<<dim3((unsigned)a.pieces), kThreads, 0, stream>>>(a);
+  } else {
+    kv8_weigh_kernel<D><<<dim3((unsigned)(a.c.R * a.c.H)), kThreads, 0, stream>>>(a);
+  }
   return hipGetLastError();
 }
 
 }  // namespace
 
+// Pieces for `items` items (at most `most`), in whose contexts the queries see
+// `span` tokens at most; `fill` workgroups fill the chip once.
+static void divide(Kv8AttendArgs& a, int64_t items, int64_t most, int64_t fill) {
+  int64_t span = a.c.max_len;
+  if (a.causal && a.window && a.window + a.n_tok + 16 < span) span = a.window + a.n_tok + 16;
+  const int64_t units = (span + kUnit - 1) / kUnit;
+  a.pieces = a.target = 0;
+  // a workgroup for each item where the contexts are short or the items many
+  if (units <= kLeast || items >= 1024 || most * units >= 0x7fffffff) return;
+  a.target = (int32_t)(items < fill ? fill - items / 2 : fill / 2);   // rounding up adds half a piece an item
+  // an item has at most one piece over its share, and none of fewer than kLeast units but the last
+  const int64_t each = (units + kLeast - 1) / kLeast;
+  a.pieces = (int32_t)(most * each < a.target + most ? most * each : a.target + most);
+}
+
 void kv8_attend_plan(Kv8AttendArgs& a) {
   const int64_t rows = a.n_tok * a.G, R = a.c.R;
   a.row_tile = rows <= 16 * R ? 16 : 32;
-  int64_t tiles = (rows + a.row_tile - 1) / a.row_tile;
-  if (tiles < R) tiles = R < a.n_tok ? R : a.n_tok;
-  int64_t span = a.c.max_len;   // tokens that one request's queries see, at most
-  if (a.causal && a.window && a.window + a.n_tok + 16 < span) span = a.window + a.n_tok + 16;
-  // a workgroup for each item where the contexts are short or the items many
-  const int64_t items = tiles * a.c.H, units = (span + kUnit - 1) / kUnit;
-  int64_t most = rows / a.row_tile + R;        // items that there may be
-  if (most > rows) most = rows;
-  most *= a.c.H;
-  a.pieces = a.target = 0;
-  if (span > kLeast * kUnit && items < 1024 && most * units < 0x7fffffff) {
-    const int64_t fill = a.row_tile == 16 ? FILL : FILL * 2 / 3;
-    a.target = (int32_t)(items < fill ? fill - items / 2 : fill / 2);   // rounding up adds half a piece an item
-    // an item has at most one piece over its share, and none of fewer than kLeast units but the last
-    const int64_t each = (units + kLeast - 1) / kLeast;
-    a.pieces = (int32_t)(most * each < a.target + most ? most * each : a.target + most);
-  } else if (a.row_tile == 32 && rows > 48 * R) {
-    a.row_tile = 64;
-  }
+  const int64_t some = R < a.n_tok ? R : a.n_tok;      // requests with queries, at most
+  const int64_t full = (rows + a.row_tile - 1) / a.row_tile, most = rows / a.row_tile + R;
+  divide(a, (full < some ? some : full) * a.c.H, (most < rows ? most : rows) * a.c.H, a.row_tile == 16 ? FILL : FILL * 2 / 3);
+  if (a.pieces == 0 && a.row_tile == 32 && rows > 48 * R) a.row_tile = 64;
   a.tiles = rows / a.row_tile + R;
+}
+
+void kv8_weigh_plan(Kv8AttendArgs& a) {
+  const int64_t some = a.c.R < a.n_tok ? a.c.R : a.n_tok;
+  a.row_tile = 0x7fffffff;     // an item has all rows of a request and head
+  divide(a, some * a.c.H, some * a.c.H, WFILL);
 }
 
 size_t kv8_attend_workspace(const Kv8AttendArgs& a) {

@@ -49,6 +49,15 @@ inline uint32_t page_magic_of(int32_t block_size) {
   return d == 1 ? 0u : (uint32_t)(((uint64_t(1) << 32) + d - 1) / d);
 }
 
+// floor(n / d) = n * magic >> shift for n < 2^31: with shift = 31 + ceil(log2 d),
+// magic = ceil(2^shift / d) < 2^32 exceeds 2^shift / d by less than one part in
+// 2^31 of it.
+inline void group_magic_of(uint32_t d, uint32_t& magic, int32_t& shift) {
+  shift = 31;
+  while ((uint64_t(1) << (shift - 31)) < d) ++shift;
+  magic = (uint32_t)(((uint64_t(1) << shift) + d - 1) / d);
+}
+
 struct Kv8StoreArgs {
   Kv8Cache c;
   const void* k;
@@ -73,6 +82,8 @@ struct Kv8AttendArgs {
   float* part;               // workspace, where contexts are cut into pieces
   int64_t n_tok;
   int32_t Hq, G, causal, window;
+  uint32_t g_magic;          // row / G, see group_magic_of
+  int32_t g_shift;
   float scale_log2;          // softmax_scale * log2(e)
   int32_t row_tile;          // rows of a workgroup
   int32_t pieces, target;    // 0: a workgroup has an item's whole context; else workgroups launched, pieces aimed at
@@ -80,6 +91,7 @@ struct Kv8AttendArgs {
 };
 // How attention is divided over workgroups: a function of the shape alone.
 void kv8_attend_plan(Kv8AttendArgs& a);
+void kv8_weigh_plan(Kv8AttendArgs& a);
 size_t kv8_attend_workspace(const Kv8AttendArgs& a);
 hipError_t launch_kv8_attend(const Kv8AttendArgs& a, hipStream_t stream);
 hipError_t launch_kv8_weigh(const Kv8AttendArgs& a, hipStream_t stream);

@@ -128,6 +128,8 @@ int check_queries(const helm_kv8_shape_t* s) {
     return fail(HELM_E_INVALID_ARG, "window=%d must be >= 0, and 0 without causal", s->window);
   if (!std::isfinite(s->softmax_scale) || !(s->softmax_scale > 0.0))
     return fail(HELM_E_INVALID_ARG, "softmax_scale must be finite and > 0 (%g)", s->softmax_scale);
+  if ((int64_t)s->n_requests * s->n_kv_heads > 0x7fffffffLL)
+    return fail(HELM_E_INVALID_ARG, "n_requests * n_kv_heads exceeds 2^31-1");
   int64_t rows = s->n_tokens;
   if (!mul_ok(rows, s->n_q_heads) || rows > 0x7fffffffLL)
     return fail(HELM_E_INVALID_ARG, "n_tokens * n_q_heads exceeds 2^31-1");
@@ -153,6 +155,7 @@ helm::Kv8AttendArgs attend_args(const helm_kv8_shape_t* s) {
   a.n_tok = s->n_tokens;
   a.Hq = s->n_q_heads;
   a.G = s->n_q_heads / s->n_kv_heads;
+  helm::group_magic_of((uint32_t)a.G, a.g_magic, a.g_shift);
   a.causal = s->causal;
   a.window = s->window;
   a.scale_log2 = (float)(s->softmax_scale * 1.4426950408889634);
@@ -161,7 +164,6 @@ helm::Kv8AttendArgs attend_args(const helm_kv8_shape_t* s) {
   // no request can hold more than its table's pages
   const int64_t room = (int64_t)s->max_blocks * s->block_size;
   if (room < a.c.max_len) a.c.max_len = (int32_t)room;
-  helm::kv8_attend_plan(a);
   return a;
 }
 
@@ -322,7 +324,9 @@ int helm_kv8_store(const void* k, const void* v, const int32_t* cu, const int32_
 size_t helm_kv8_attend_workspace_bytes(const helm_kv8_shape_t* s) {
   clear_error();
   if (check_kv8(s) != HELM_OK || check_queries(s) != HELM_OK) return 0;
-  const size_t n = helm::kv8_attend_workspace(attend_args(s));
+  helm::Kv8AttendArgs a = attend_args(s);
+  helm::kv8_attend_plan(a);
+  const size_t n = helm::kv8_attend_workspace(a);
   return n ? align_up(n) : kAlign;
 }
 
@@ -342,6 +346,7 @@ int helm_kv8_attend(const void* q, const int32_t* cu, const int32_t* kv_len, con
       (rc = check_aligned(v_pool, "v_pool", 16)) || (rc = check_aligned(out, "out", 16)))
     return rc;
   helm::Kv8AttendArgs a = attend_args(s);
+  helm::kv8_attend_plan(a);
   if (a.tiles * s->n_kv_heads > 0x7fffffffLL)
     return fail(HELM_E_INVALID_ARG, "%lld row tiles of %d KV heads exceed 2^31-1", (long long)a.tiles, s->n_kv_heads);
   const size_t need = helm::kv8_attend_workspace(a);
@@ -387,6 +392,7 @@ int helm_kv8_weigh(const void* q, const float* lse, const int32_t* cu, const int
   rc = device_gate(-1);
   if (rc != HELM_OK) return rc;
   helm::Kv8AttendArgs a = attend_args(s);
+  helm::kv8_weigh_plan(a);
   const int32_t longest = a.c.max_len;
   a.c = cache_of(s, k_pool, nullptr, k_scale, nullptr, table);
   a.c.max_len = longest;
