@@ -565,22 +565,45 @@ def _bind_serving(L):
     L.helm_kv8_evict_check.argtypes = [P(HelmKv8EvictShape)] + [vp] * 3
 
 
+# A decode step makes these calls once a layer: what a call checks is read from
+# each tensor once, and the messages are made only for a tensor that fails.
+def _ptr(t, name, dtype, shape):
+    """Address of a contiguous GPU tensor of this type and shape."""
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    return _dev_ptr(t, name, dtype, shape)
+
+
 def _heads_ptr(t, name, dtype, shape):
-    """Address of a [tokens, heads, dim] tensor of any token and head strides
-    whose heads are contiguous; strides come back with it."""
+    """Address of a [tokens, heads, dim] GPU tensor of any token and head
+    strides whose heads are contiguous; the two strides come back with it."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must live on the GPU (got {t.device})")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     tok, head, one = t.stride()
     if one != 1:
         raise ValueError(f"the values of a head of {name} must be contiguous (strides {t.stride()})")
-    return t.data_ptr(), max(tok, 1), max(head, 1)
+    return t.data_ptr(), tok or 1, head or 1
+
+
+def _stream_of(t):
+    """torch's current stream on a tensor's GPU, as a hipStream_t."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _serving_shape(shape, t):
+    """A copy of the caller's shape for one call, its stream resolved as in _call_shape."""
+    s = type(shape).from_buffer_copy(shape)
+    if not s.stream:
+        s.stream = _stream_of(t)
+    return s
 
 
 def make_rope(head_dim: int, theta: float, rot_dim: int = None, layout: int = HELM_ROPE_HALF,
@@ -604,27 +627,28 @@ def helm_rope(q, k, pos, rope: HelmRope, mode: int = HELM_ROPE_FORWARD, out_q=No
     x = q if q is not None else k
     if x is None:
         raise ValueError("q or k must be given")
-    s = HelmRopeShape(dtype=_dtype_code(x), mode=mode)
-    N, D = x.shape[0], x.shape[2]
+    N, _, D = x.shape
+    dt = x.dtype
+    s = HelmRopeShape(0, 0, _dtype_code(x), mode, N)
     if D != rope.head_dim:
         raise ValueError(f"heads of {D} values, but the plan is for head_dim {rope.head_dim}")
-    ptrs = [None, None, None, None]
+    qp = kp = oqp = okp = None
     if q is not None:
         if out_q is None:
-            out_q = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            out_q = torch.empty(q.shape, dtype=dt, device=q.device)
+        shape = (N, q.shape[1], D)
         s.n_q_heads = q.shape[1]
-        ptrs[0], s.q_tok, s.q_head = _heads_ptr(q, "q", x.dtype, (N, q.shape[1], D))
-        ptrs[2], s.out_q_tok, s.out_q_head = _heads_ptr(out_q, "out_q", x.dtype, (N, q.shape[1], D))
+        qp, s.q_tok, s.q_head = _heads_ptr(q, "q", dt, shape)
+        oqp, s.out_q_tok, s.out_q_head = _heads_ptr(out_q, "out_q", dt, shape)
     if k is not None:
         if out_k is None:
-            out_k = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            out_k = torch.empty(k.shape, dtype=dt, device=k.device)
+        shape = (N, k.shape[1], D)
         s.n_k_heads = k.shape[1]
-        ptrs[1], s.k_tok, s.k_head = _heads_ptr(k, "k", x.dtype, (N, k.shape[1], D))
-        ptrs[3], s.out_k_tok, s.out_k_head = _heads_ptr(out_k, "out_k", x.dtype, (N, k.shape[1], D))
-    s.n_tokens = N
-    s.stream = current_stream_ptr(x.device) or None
-    _raise(lib().helm_rope(ptrs[0], ptrs[1], _dev_ptr(pos, "pos", torch.int32, (N,)), ptrs[2], ptrs[3],
-                           ctypes.byref(rope), ctypes.byref(s)))
+        kp, s.k_tok, s.k_head = _heads_ptr(k, "k", dt, shape)
+        okp, s.out_k_tok, s.out_k_head = _heads_ptr(out_k, "out_k", dt, shape)
+    s.stream = _stream_of(x)
+    _raise(lib().helm_rope(qp, kp, _ptr(pos, "pos", torch.int32, (N,)), oqp, okp, ctypes.byref(rope), ctypes.byref(s)))
     return out_q, out_k
 
 
@@ -645,20 +669,20 @@ def _kv8_ptrs(s, k_pool, v_pool, k_scale, v_scale):
     import torch
     pool = (s.n_blocks, s.n_kv_heads, s.block_size, s.head_dim)
     scale = (s.n_blocks, s.n_kv_heads)
-    return [_dev_ptr(k_pool, "k_pool", torch.float8_e4m3fn, pool), _dev_ptr(v_pool, "v_pool", torch.float8_e4m3fn, pool),
-            _dev_ptr(k_scale, "k_scale", torch.float32, scale), _dev_ptr(v_scale, "v_scale", torch.float32, scale)]
+    return (_ptr(k_pool, "k_pool", torch.float8_e4m3fn, pool), _ptr(v_pool, "v_pool", torch.float8_e4m3fn, pool),
+            _ptr(k_scale, "k_scale", torch.float32, scale), _ptr(v_scale, "v_scale", torch.float32, scale))
 
 
 def _kv8_tables(s, cu_seqlens, lens, block_table, name):
     import torch
     R = s.n_requests
-    return [_dev_ptr(cu_seqlens, "cu_seqlens", torch.int32, (R + 1,)), _dev_ptr(lens, name, torch.int32, (R,)),
-            _dev_ptr(block_table, "block_table", torch.int32, (R, s.max_blocks))]
+    return (_ptr(cu_seqlens, "cu_seqlens", torch.int32, (R + 1,)), _ptr(lens, name, torch.int32, (R,)),
+            _ptr(block_table, "block_table", torch.int32, (R, s.max_blocks)))
 
 
 def _kv8_weights(s, weights):
     import torch
-    return _dev_ptr(weights, "weights", torch.float32, (s.n_blocks, s.n_kv_heads, s.block_size))
+    return _ptr(weights, "weights", torch.float32, (s.n_blocks, s.n_kv_heads, s.block_size))
 
 
 def helm_kv8_store(k, v, cu_seqlens, kv_start, block_table, k_pool, v_pool, k_scale, v_scale, shape: HelmKv8Shape,
@@ -666,7 +690,7 @@ def helm_kv8_store(k, v, cu_seqlens, kv_start, block_table, k_pool, v_pool, k_sc
     """New tokens k, v [n_tokens, H, D] (bf16 or fp32, any token and head
     strides) into the 8-bit cache, behind each request's kv_start tokens.
     ``weights``: the accumulated weights, zeroed for the stored tokens."""
-    s = _call_shape(shape, k_pool.device)
+    s = _serving_shape(shape, k_pool)
     s.dtype = _dtype_code(k)
     nhd = (s.n_tokens, s.n_kv_heads, s.head_dim)
     kp, s.tok_stride, s.head_stride = _heads_ptr(k, "k", k.dtype, nhd)
@@ -690,7 +714,7 @@ def helm_kv8_attend(q, cu_seqlens, kv_len, block_table, k_pool, v_pool, k_scale,
     fp32), allocated where not given; so is the workspace
     (helm_kv8_attend_workspace_bytes)."""
     import torch
-    s = _call_shape(shape, k_pool.device)
+    s = _serving_shape(shape, k_pool)
     s.dtype = HELM_BF16
     nhd = (s.n_tokens, s.n_q_heads, s.head_dim)
     qp, s.tok_stride, s.head_stride = _heads_ptr(q, "q", torch.bfloat16, nhd)
@@ -699,11 +723,15 @@ def helm_kv8_attend(q, cu_seqlens, kv_len, block_table, k_pool, v_pool, k_scale,
     if lse is None:
         lse = torch.empty(nhd[:2], dtype=torch.float32, device=q.device)
     if workspace is None:
-        workspace = _own_workspace(helm_kv8_attend_workspace_bytes(s), q.device, s.stream)
-    s.workspace, s.workspace_bytes = _workspace_ptr(workspace, q.device)
+        n = helm_kv8_attend_workspace_bytes(s)
+        workspace = (torch.empty(n, dtype=torch.uint8, device=q.device) if not shape.stream
+                     else _own_workspace(n, q.device, s.stream))
+        s.workspace, s.workspace_bytes = workspace.data_ptr(), n
+    else:
+        s.workspace, s.workspace_bytes = _workspace_ptr(workspace, q.device)
     _raise(lib().helm_kv8_attend(qp, *_kv8_tables(s, cu_seqlens, kv_len, block_table, "kv_len"),
                                  *_kv8_ptrs(s, k_pool, v_pool, k_scale, v_scale),
-                                 _dev_ptr(out, "out", torch.bfloat16, nhd), _dev_ptr(lse, "lse", torch.float32, nhd[:2]),
+                                 _ptr(out, "out", torch.bfloat16, nhd), _ptr(lse, "lse", torch.float32, nhd[:2]),
                                  ctypes.byref(s)))
     return out, lse
 
@@ -712,12 +740,12 @@ def helm_kv8_weigh(q, lse, cu_seqlens, kv_len, block_table, k_pool, k_scale, wei
     """Adds to weights [n_blocks, H, B] the softmax weight that these queries
     give each cached token; lse as helm_kv8_attend returned it."""
     import torch
-    s = _call_shape(shape, k_pool.device)
+    s = _serving_shape(shape, k_pool)
     s.dtype = HELM_BF16
     nhd = (s.n_tokens, s.n_q_heads, s.head_dim)
     qp, s.tok_stride, s.head_stride = _heads_ptr(q, "q", torch.bfloat16, nhd)
     kp, _, ks, _ = _kv8_ptrs(s, k_pool, k_pool, k_scale, k_scale)
-    _raise(lib().helm_kv8_weigh(qp, _dev_ptr(lse, "lse", torch.float32, nhd[:2]),
+    _raise(lib().helm_kv8_weigh(qp, _ptr(lse, "lse", torch.float32, nhd[:2]),
                                 *_kv8_tables(s, cu_seqlens, kv_len, block_table, "kv_len"), kp, ks,
                                 _kv8_weights(s, weights), ctypes.byref(s)))
 
@@ -738,18 +766,18 @@ def helm_kv8_evict(weights, kv_len, src_block_table, dst_block_table, k_pool, v_
     copied in order into the blocks of dst_block_table (weights too).  Returns
     (kept [R, H, budget] int32, new_len [R] int32)."""
     import torch
-    s = _call_shape(shape, k_pool.device)
+    s = _serving_shape(shape, k_pool)
     R, H = s.n_requests, s.n_kv_heads
     if kept is None:
         kept = torch.empty((R, H, s.budget), dtype=torch.int32, device=k_pool.device)
     if new_len is None:
         new_len = torch.empty((R,), dtype=torch.int32, device=k_pool.device)
-    _raise(lib().helm_kv8_evict(_dev_ptr(kv_len, "kv_len", torch.int32, (R,)),
-                                _dev_ptr(src_block_table, "src_block_table", torch.int32, (R, s.max_blocks_src)),
-                                _dev_ptr(dst_block_table, "dst_block_table", torch.int32, (R, s.max_blocks_dst)),
+    _raise(lib().helm_kv8_evict(_ptr(kv_len, "kv_len", torch.int32, (R,)),
+                                _ptr(src_block_table, "src_block_table", torch.int32, (R, s.max_blocks_src)),
+                                _ptr(dst_block_table, "dst_block_table", torch.int32, (R, s.max_blocks_dst)),
                                 *_kv8_ptrs(s, k_pool, v_pool, k_scale, v_scale), _kv8_weights(s, weights),
-                                _dev_ptr(kept, "kept", torch.int32, (R, H, s.budget)),
-                                _dev_ptr(new_len, "new_len", torch.int32, (R,)), ctypes.byref(s)))
+                                _ptr(kept, "kept", torch.int32, (R, H, s.budget)),
+                                _ptr(new_len, "new_len", torch.int32, (R,)), ctypes.byref(s)))
     return kept, new_len
 
 
