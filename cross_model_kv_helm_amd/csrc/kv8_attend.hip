@@ -32,6 +32,9 @@
 namespace helm {
 namespace {
 
+#ifndef PT
+#define PT 64
+#endif
 #ifndef WA
 #define WA 2
 #endif
@@ -198,24 +201,12 @@ __device__ __forceinline__ void load_v(const Kv8Cache& c, const Tile& x, int g, 
 
 // One row tile's probabilities (times the value's scale) of 32 tokens from
 // their raw scores; rescales l and o where the reference moves.
-template <int D, bool MASK>
+template <int D>
 __device__ __forceinline__ bf16x8 probabilities(const f32x4 (&s)[2], const float (&ks)[2], const float (&lv)[2],
-                                                const float (&inv)[2], const Seen& see, int tok, float& mref, float& l,
-                                                f32x4 (&o)[D / 16]) {
-  float y[8], top[2];
+                                                const float (&inv)[2], float& mref, float& l, f32x4 (&o)[D / 16]) {
+  float top[2];
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    if constexpr (MASK) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = tok + 16 * u + i;
-        y[4 * u + i] = t < see.lo || t >= see.hi ? -INFINITY : s[u][i] * ks[u];
-      }
-      top[u] = fmaxf(fmaxf(y[4 * u], y[4 * u + 1]), fmaxf(y[4 * u + 2], y[4 * u + 3]));
-    } else {
-      top[u] = fmaxf(fmaxf(s[u][0], s[u][1]), fmaxf(s[u][2], s[u][3])) * ks[u];
-    }
-  }
+  for (int u = 0; u < 2; ++u) top[u] = fmaxf(fmaxf(s[u][0], s[u][1]), fmaxf(s[u][2], s[u][3])) * ks[u];
   float t = fmaxf(top[0], top[1]);
   if (__any(t > mref + kLazy)) {
     t = fmaxf(t, __shfl_xor(t, 16));
@@ -234,7 +225,7 @@ __device__ __forceinline__ bf16x8 probabilities(const f32x4 (&s)[2], const float
     float e[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      e[i] = __builtin_amdgcn_exp2f(MASK ? y[4 * u + i] + down : fmaf(s[u][i], ks[u], down));
+      e[i] = __builtin_amdgcn_exp2f(fmaf(s[u][i], ks[u], down));
       p[4 * u + i] = (__bf16)e[i];
     }
     l = fmaf((e[0] + e[1]) + (e[2] + e[3]), inv[u], l);
@@ -288,7 +279,10 @@ template <int D, int MT, int RG>
 struct AttendLds {
   static constexpr int TG = kWaves / RG, PAD = D + 4;
   static constexpr int kJoinRows = TG == 4 ? 16 * MT : TG == 2 ? 8 * MT : 1;   // of a wave, exchanged at the end
-  float o[kWaves][kJoinRows][PAD];
+  union {
+    float o[kWaves][kJoinRows][PAD];
+    u32x4 q[MT > 2 ? RG * MT * (D / 32) * 64 : 1];
+  };
   float m[kWaves][16 * MT], l[kWaves][16 * MT];
 };
 
@@ -304,14 +298,25 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
   const int row0 = st.tile * TR, rowg = row0 + 16 * MT * rg;      // the workgroup's, this wave's
   const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
 
-  bf16x8 qv[MT][KS];
+  constexpr bool QL = MT > 2;
+  bf16x8 qv[QL ? 1 : MT][KS];
   Seen see[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
     const int row = min(rowg + 16 * t + m, M - 1);
     see[t] = seen_by(a, q, query_of(a, row));
-    load_q<D>(a, q, h, row, g, qv[t]);
+    if constexpr (QL) {
+      if (t / (MT / TG) == tg) {
+        bf16x8 v[KS];
+        load_q<D>(a, q, h, row, g, v);
+#pragma unroll
+        for (int i = 0; i < KS; ++i) lds.q[((rg * MT + t) * KS + i) * 64 + lane] = __builtin_bit_cast(u32x4, v[i]);
+      }
+    } else {
+      load_q<D>(a, q, h, row, g, qv[t]);
+    }
   }
+  if constexpr (QL) __syncthreads();
   const int last = min(rowg + 16 * MT, M) - 1;
   const Seen s_first = seen_by(a, q, min(rowg, M - 1) / a.G), s_last = seen_by(a, q, last / a.G);
   // a wave of a row group that has no rows left (rowg >= M) finds begin >= end
@@ -336,7 +341,7 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
   const auto scales = [&](const Tile (&x)[2], float (&ks)[2], float (&vs)[2]) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      ks[u] = c.k_scale[x[u].slab] * a.scale_log2;
+      ks[u] = fmaxf(c.k_scale[x[u].slab] * a.scale_log2, 1.17549435e-38f);
       vs[u] = c.v_scale[x[u].slab];
     }
   };
@@ -364,9 +369,12 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
       for (int u = 0; u < 2; ++u) k[u] = cvt8(w.k[u][i / 2][2 * (i & 1)], w.k[u][i / 2][2 * (i & 1) + 1]);
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
-        s[t][0] = mfma(k[0], qv[t][i], s[t][0]);
-        s[t][1] = mfma(k[1], qv[t][i], s[t][1]);
+        bf16x8 qq;
+        if constexpr (QL) qq = __builtin_bit_cast(bf16x8, lds.q[((rg * MT + t) * KS + i) * 64 + lane]); else qq = qv[t][i];
+        s[t][0] = mfma(k[0], qq, s[t][0]);
+        s[t][1] = mfma(k[1], qq, s[t][1]);
       }
+      if constexpr (QL) __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u) load_k<D>(c, next.x[u], g, m, w.k[u]);
@@ -399,22 +407,24 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
       lv[u] = __builtin_amdgcn_logf(now.vs[u]);
       inv[u] = __builtin_amdgcn_rcpf(now.vs[u]);
     }
+    // masked scores become -inf here (their factor is positive), so that what
+    // follows is one path: a second one cost 60 registers
+    if (t0 < s_last.lo || t0 + kStep > s_first.hi || !there) {
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int tok = t0 + 16 * u + 4 * g + i;
+            if (!now.x[u].ok || tok < see[t].lo || tok >= see[t].hi) s[t][u][i] = -INFINITY;
+          }
+    }
     bf16x8 pv[MT];
-    if (t0 >= s_last.lo && t0 + kStep <= s_first.hi && there) {
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
-        pv[t] = probabilities<D, false>(s[t], now.ks, lv, inv, see[t], 0, mref[t], l[t], o[t]);
-    } else {
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-        if (!now.x[u].ok) {
-#pragma unroll
-          for (int t = 0; t < MT; ++t) s[t][u] = f32x4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          now.ks[u] = 1.0f;
-        }
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-        pv[t] = probabilities<D, true>(s[t], now.ks, lv, inv, see[t], t0 + 4 * g, mref[t], l[t], o[t]);
+    for (int t = 0; t < MT; ++t) {
+      pv[t] = probabilities<D>(s[t], now.ks, lv, inv, mref[t], l[t], o[t]);
+      if constexpr (QL) __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int b = 0; b < D / 64; ++b) {
@@ -426,6 +436,7 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
         const bf16x8 v = cvt8(w0[j], w1[j]);
 #pragma unroll
         for (int t = 0; t < MT; ++t) o[t][4 * b + j] = mfma(v, pv[t], o[t][4 * b + j]);
+        if constexpr (QL) { if (j & 1) __builtin_amdgcn_sched_barrier(0); }
       }
     }
 #pragma unroll
@@ -460,6 +471,7 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
         write_row<D>(a, row_at(rowg + 16 * t + m), st.piece, rowg - row0 + 16 * t + m, g, mref[t], l[t], o[t]);
   } else if constexpr (TG == 2) {   // each of the two finishes half of the row tiles
     constexpr int HT = MT / 2;
+    if constexpr (QL) __syncthreads();
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       if (g == 0) {
@@ -911,7 +923,9 @@ template <int D>
 hipError_t attend(const Kv8AttendArgs& a, hipStream_t stream) {
   if (a.pieces == 0) {
     const dim3 grid((unsigned)(a.tiles * a.c.H));
-    if (a.row_tile == 64)
+    if (a.row_tile == 128)
+      kv8_attend_kernel<D, 4, 2><<<grid, kThreads, 0, stream>>>(a);
+    else if (a.row_tile == 64)
       kv8_attend_kernel<D, 2, 2><<<grid, kThreads, 0, stream>>>(a);
     else if (a.row_tile == 32)
       kv8_attend_kernel<D, 2, 1><<<grid, kThreads, 0, stream>>>(a);
@@ -965,7 +979,7 @@ void kv8_attend_plan(Kv8AttendArgs& a) {
   const int64_t some = R < a.n_tok ? R : a.n_tok;      // requests with queries, at most
   const int64_t full = (rows + a.row_tile - 1) / a.row_tile, most = rows / a.row_tile + R;
   divide(a, (full < some ? some : full) * a.c.H, (most < rows ? most : rows) * a.c.H, a.row_tile == 16 ? FILL : FILL * 2 / 3);
-  if (a.pieces == 0 && a.row_tile == 32 && rows > 48 * R) a.row_tile = 64;
+  if (a.pieces == 0 && a.row_tile == 32 && rows > 48 * R) a.row_tile = PT;
   a.tiles = rows / a.row_tile + R;
 }
 
