@@ -10,8 +10,8 @@
 // tokens of one query row, which is where the second product, O^T = V^T P^T,
 // takes its right operand from — P never leaves the registers.  The order of
 // the contracted index is free as long as both operands agree, so
-//   - lane (g, m) of a wave (g = lane / 16, m = lane % 16) loads the D/4
-//     consecutive codes d = g*D/4.. of token m of a 16-token tile for S^T, and
+//   - lane (g, m) of a wave (g = lane / 16, m = lane % 16) loads the 16 codes
+//     d = 64i + 16g.. of token m of a 16-token tile for S^T, and
 //   - codes d = m*D/16.. of tokens 4g..4g+3 of two tiles for O^T, whose 4x4
 //     byte blocks it transposes in registers (v_perm): output row m of the
 //     j-th product is d = m*D/16 + j.
@@ -33,7 +33,7 @@ namespace helm {
 namespace {
 
 #ifndef PT
-#define PT 64
+#define PT 128
 #endif
 #ifndef WA
 #define WA 2
@@ -113,14 +113,15 @@ __device__ __forceinline__ Tile tile_at(const Kv8Cache& c, const int32_t* row, i
   return x;
 }
 
-// Keys of a tile: this lane's D/4 codes.  (A uniform base and a 32-bit lane
+// Keys of a tile: this lane's D/4 codes, 64 consecutive ones of a token by the
+// four lanes that share it (pieces 32 apart took twice the cache accesses).  (A uniform base and a 32-bit lane
 // offset: one address register.)
 template <int D>
 __device__ __forceinline__ void load_k(const Kv8Cache& c, const Tile& x, int g, int m, u32x4 (&w)[D / 64]) {
   const uint8_t* p = c.k_pool + (x.slab * c.B + x.off) * D;
-  const uint32_t lane = m * D + g * (D / 4);
+  const uint32_t lane = m * D + g * 16;
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i) w[i] = *(const u32x4*)(p + lane + 16 * i);
+  for (int i = 0; i < D / 64; ++i) w[i] = *(const u32x4*)(p + lane + 64 * i);
 }
 
 // Query of a row: row / G as a 64-bit product, see group_magic_of.
@@ -128,14 +129,14 @@ __device__ __forceinline__ int query_of(const Kv8AttendArgs& a, int row) {
   return (int)((uint64_t)(uint32_t)row * a.g_magic >> a.g_shift);
 }
 
-// 16 queries as the right operand of S^T: this lane's row, d = g*D/4 + 8s.
+// 16 queries as the right operand of S^T: this lane's row, the d of its codes.
 template <int D>
 __device__ __forceinline__ void load_q(const Kv8AttendArgs& a, const Request& q, int h, int row, int g,
                                        bf16x8 (&v)[D / 32]) {
   const int i = query_of(a, row);
-  const uint16_t* p = a.q + (q.c0 + i) * a.q_tok + (int64_t)(h * a.G + row - i * a.G) * a.q_head + g * (D / 4);
+  const uint16_t* p = a.q + (q.c0 + i) * a.q_tok + (int64_t)(h * a.G + row - i * a.G) * a.q_head + g * 16;
 #pragma unroll
-  for (int s = 0; s < D / 32; ++s) __builtin_memcpy(&v[s], p + 8 * s, 16);
+  for (int s = 0; s < D / 32; ++s) __builtin_memcpy(&v[s], p + 64 * (s >> 1) + 8 * (s & 1), 16);
 }
 
 template <int D>
@@ -436,7 +437,6 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
         const bf16x8 v = cvt8(w0[j], w1[j]);
 #pragma unroll
         for (int t = 0; t < MT; ++t) o[t][4 * b + j] = mfma(v, pv[t], o[t][4 * b + j]);
-        if constexpr (QL) { if (j & 1) __builtin_amdgcn_sched_barrier(0); }
       }
     }
 #pragma unroll
@@ -712,9 +712,9 @@ template <int D>
 __device__ __forceinline__ void load_rows(const Kv8AttendArgs& a, const Request& q, int h, int row0, int g, int m,
                                           RowTile<D>& x) {
   const int row = min(row0 + m, q.n * a.G - 1), i = query_of(a, row), head = h * a.G + row - i * a.G;
-  const uint16_t* p = a.q + (q.c0 + i) * a.q_tok + head * a.q_head + g * (D / 4);
+  const uint16_t* p = a.q + (q.c0 + i) * a.q_tok + head * a.q_head + g * 16;
 #pragma unroll
-  for (int s = 0; s < D / 32; ++s) __builtin_memcpy(&x.q[s], p + 8 * s, 16);
+  for (int s = 0; s < D / 32; ++s) __builtin_memcpy(&x.q[s], p + 64 * (s >> 1) + 8 * (s & 1), 16);
   x.lse = a.lse[(q.c0 + i) * a.Hq + head];
 }
 // lse of rows 4g..4g+3 in units of log2; a row past the end, or whose lse is
