@@ -99,18 +99,23 @@ struct Tile {
   int off;           // first slot
   bool ok;           // inside the context, in a block of the pool
 };
-__device__ __forceinline__ Tile tile_at(const Kv8Cache& c, const int32_t* row, int h, int t, int len) {
+// Its table entry, read early (of the last token's page where t is past it) ...
+__device__ __forceinline__ int entry_at(const Kv8Cache& c, const int32_t* row, int t, int len) {
+  const int s = max(min(t, len - 1), 0);
+  return row[c.page_magic ? (int)__umulhi((uint32_t)s >> 4, c.page_magic) : s >> 4];
+}
+// ... and what it says, once it is there.
+__device__ __forceinline__ Tile tile_of(const Kv8Cache& c, int entry, int h, int t, int len) {
   Tile x;
   const int page = c.page_magic ? (int)__umulhi((uint32_t)t >> 4, c.page_magic) : t >> 4;
-  x.ok = t < len;
-  int blk = 0;
-  if (x.ok) blk = row[page];
-  x.ok = x.ok && (uint32_t)blk < (uint32_t)c.n_blocks;
-  blk = __builtin_amdgcn_readfirstlane(x.ok ? blk : 0);
-  x.slab = (int64_t)blk * c.H + h;
-  x.off = t - page * c.B;
-  if (!x.ok) x.off = 0;
+  const int blk = __builtin_amdgcn_readfirstlane(entry);
+  x.ok = t < len && (uint32_t)blk < (uint32_t)c.n_blocks;
+  x.slab = (int64_t)(x.ok ? blk : 0) * c.H + h;
+  x.off = x.ok ? t - page * c.B : 0;
   return x;
+}
+__device__ __forceinline__ Tile tile_at(const Kv8Cache& c, const int32_t* row, int h, int t, int len) {
+  return tile_of(c, entry_at(c, row, t, len), h, t, len);
 }
 
 // Keys of a tile: this lane's D/4 codes, 64 consecutive ones of a token by the
@@ -335,29 +340,29 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
   }
 
   const int32_t* table = c.table + (int64_t)q.r * c.max_blocks;
-  const auto tiles = [&](int t, Tile (&x)[2]) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) x[u] = tile_at(c, table, h, t + 16 * u, min(end, q.len));
-  };
-  const auto scales = [&](const Tile (&x)[2], float (&ks)[2], float (&vs)[2]) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      ks[u] = fmaxf(c.k_scale[x[u].slab] * a.scale_log2, 1.17549435e-38f);
-      vs[u] = c.v_scale[x[u].slab];
-    }
-  };
+  const int limit = min(end, q.len);
   constexpr int kStride = TG * kStep;
   int t0 = begin + tg * kStep;
   Codes<D> w;
   Pages now, next;
-  Tile after[2];
-  tiles(t0, now.x);
-  tiles(t0 + kStride, next.x);
+  int entry[2];
+  // scales as loaded: they are made use of a step later
+  const auto fetch_k = [&](int t, Pages& p) {
 #pragma unroll
-  for (int u = 0; u < 2; ++u) load_k<D>(c, now.x[u], g, m, w.k[u]);
+    for (int u = 0; u < 2; ++u) {
+      p.x[u] = tile_of(c, entry[u], h, t + 16 * u, limit);
+      load_k<D>(c, p.x[u], g, m, w.k[u]);
+      p.ks[u] = c.k_scale[p.x[u].slab];
+      p.vs[u] = c.v_scale[p.x[u].slab];
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) entry[u] = entry_at(c, table, t + kStride + 16 * u, limit);
+  };
+#pragma unroll
+  for (int u = 0; u < 2; ++u) entry[u] = entry_at(c, table, t0 + 16 * u, limit);
+  fetch_k(t0, now);
 #pragma unroll
   for (int u = 0; u < 2; ++u) load_v<D>(c, now.x[u], g, m, w.v[u]);
-  scales(now.x, now.ks, now.vs);
 
   for (; t0 < end; t0 += kStride) {
     f32x4 s[MT][2];
@@ -377,10 +382,7 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
       }
       if constexpr (QL) __builtin_amdgcn_sched_barrier(0);
     }
-#pragma unroll
-    for (int u = 0; u < 2; ++u) load_k<D>(c, next.x[u], g, m, w.k[u]);
-    scales(next.x, next.ks, next.vs);
-    tiles(t0 + 2 * kStride, after);
+    fetch_k(t0 + kStride, next);
 
     float lv[2], inv[2];
     bool odd = t0 + kStep > q.len, there = true;
@@ -405,6 +407,7 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
+      now.ks[u] = fmaxf(now.ks[u] * a.scale_log2, 1.17549435e-38f);
       lv[u] = __builtin_amdgcn_logf(now.vs[u]);
       inv[u] = __builtin_amdgcn_rcpf(now.vs[u]);
     }
@@ -442,8 +445,6 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
 #pragma unroll
     for (int u = 0; u < 2; ++u) load_v<D>(c, next.x[u], g, m, w.v[u]);
     now = next;
-#pragma unroll
-    for (int u = 0; u < 2; ++u) next.x[u] = after[u];
   }
 
   // join the waves of a row group: lane (g, m) has row m, d = g*D/4 + (D/16)*i + j
@@ -782,21 +783,24 @@ __device__ __forceinline__ void weigh_stretch(const Kv8AttendArgs& a, const Requ
   load_rows<D>(a, q, h, 0, g, m, rows);
   row_lse(rows.lse, m < M, g, lse);
   const Seen s_first = seen_by(a, q, 0), s_last = seen_by(a, q, query_of(a, min(16, M) - 1));
-  const auto tiles = [&](int t, Tile (&x)[2]) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) x[u] = tile_at(c, table, h, t + 16 * u, to);
-  };
   int t0 = from + wave * kStep;
   Tile now[2], next[2];
   u32x4 kw[2][D / 64];
   float ks[2];
-  tiles(t0, now);
-  tiles(t0 + kUnit, next);
+  int entry[2];
+  const auto fetch = [&](int t, Tile (&x)[2]) {
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    load_k<D>(c, now[u], g, m, kw[u]);
-    ks[u] = c.k_scale[now[u].slab];
-  }
+    for (int u = 0; u < 2; ++u) {
+      x[u] = tile_of(c, entry[u], h, t + 16 * u, to);
+      load_k<D>(c, x[u], g, m, kw[u]);
+      ks[u] = c.k_scale[x[u].slab];
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) entry[u] = entry_at(c, table, t + kUnit + 16 * u, to);
+  };
+#pragma unroll
+  for (int u = 0; u < 2; ++u) entry[u] = entry_at(c, table, t0 + 16 * u, to);
+  fetch(t0, now);
   for (; t0 < to; t0 += kUnit) {
     bf16x8 k[2][D / 32];
     float scale[2], was = 0.0f;
@@ -804,11 +808,8 @@ __device__ __forceinline__ void weigh_stretch(const Kv8AttendArgs& a, const Requ
     for (int u = 0; u < 2; ++u) {
       convert_k<D>(kw[u], k[u]);
       scale[u] = ks[u] * a.scale_log2;
-      load_k<D>(c, next[u], g, m, kw[u]);
-      ks[u] = c.k_scale[next[u].slab];
     }
-    Tile after[2];
-    tiles(t0 + 2 * kUnit, after);
+    fetch(t0 + kUnit, next);
     const int tok = t0 + lane;                  // of the 32, by lanes 0..31
     const Tile& mine = g == 1 ? now[1] : now[0];
     float* w = a.weights + mine.slab * c.B + mine.off + m;
@@ -830,10 +831,7 @@ __device__ __forceinline__ void weigh_stretch(const Kv8AttendArgs& a, const Requ
     }
     if (own) *w = was + (g == 0 ? acc[0] : acc[1]);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      now[u] = next[u];
-      next[u] = after[u];
-    }
+    for (int u = 0; u < 2; ++u) now[u] = next[u];
   }
 }
 
