@@ -35,9 +35,6 @@ namespace {
 #ifndef PT
 #define PT 128
 #endif
-#ifndef WA
-#define WA 2
-#endif
 #ifndef WFILL
 #define WFILL 768
 #endif
@@ -366,6 +363,7 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
 
   for (; t0 < end; t0 += kStride) {
     f32x4 s[MT][2];
+    if constexpr (QL) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int t = 0; t < MT; ++t) s[t][0] = s[t][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -380,8 +378,9 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
         s[t][0] = mfma(k[0], qq, s[t][0]);
         s[t][1] = mfma(k[1], qq, s[t][1]);
       }
-      if constexpr (QL) __builtin_amdgcn_sched_barrier(0);
+      if constexpr (QL) __builtin_amdgcn_sched_barrier(0x100);
     }
+    if constexpr (QL) __builtin_amdgcn_s_setprio(0);
     fetch_k(t0 + kStride, next);
 
     float lv[2], inv[2];
@@ -428,8 +427,9 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       pv[t] = probabilities<D>(s[t], now.ks, lv, inv, mref[t], l[t], o[t]);
-      if constexpr (QL) __builtin_amdgcn_sched_barrier(0);
+      if constexpr (QL) __builtin_amdgcn_sched_barrier(0x100);
     }
+    if constexpr (QL) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int b = 0; b < D / 64; ++b) {
       uint32_t w0[4], w1[4];
@@ -444,6 +444,7 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u) load_v<D>(c, next.x[u], g, m, w.v[u]);
+    if constexpr (QL) __builtin_amdgcn_s_setprio(0);
     now = next;
   }
 
@@ -709,13 +710,15 @@ struct RowTile {     // 16 rows, as loaded: this lane's operand and lse are row 
   bf16x8 q[D / 32];
   float lse;
 };
-template <int D>
+// PLAIN: product s contracts d = 32s + 8g.., whose queries four lanes load side
+// by side; else the d that load_k gives each lane.
+template <int D, bool PLAIN>
 __device__ __forceinline__ void load_rows(const Kv8AttendArgs& a, const Request& q, int h, int row0, int g, int m,
                                           RowTile<D>& x) {
   const int row = min(row0 + m, q.n * a.G - 1), i = query_of(a, row), head = h * a.G + row - i * a.G;
-  const uint16_t* p = a.q + (q.c0 + i) * a.q_tok + head * a.q_head + g * 16;
+  const uint16_t* p = a.q + (q.c0 + i) * a.q_tok + head * a.q_head + g * (PLAIN ? 8 : 16);
 #pragma unroll
-  for (int s = 0; s < D / 32; ++s) __builtin_memcpy(&x.q[s], p + 64 * (s >> 1) + 8 * (s & 1), 16);
+  for (int s = 0; s < D / 32; ++s) __builtin_memcpy(&x.q[s], p + (PLAIN ? 32 * s : 64 * (s >> 1) + 8 * (s & 1)), 16);
   x.lse = a.lse[(q.c0 + i) * a.Hq + head];
 }
 // lse of rows 4g..4g+3 in units of log2; a row past the end, or whose lse is
@@ -780,7 +783,7 @@ __device__ __forceinline__ void weigh_stretch(const Kv8AttendArgs& a, const Requ
   const int32_t* table = c.table + (int64_t)q.r * c.max_blocks;
   RowTile<D> rows;
   float lse[4];
-  load_rows<D>(a, q, h, 0, g, m, rows);
+  load_rows<D, false>(a, q, h, 0, g, m, rows);
   row_lse(rows.lse, m < M, g, lse);
   const Seen s_first = seen_by(a, q, 0), s_last = seen_by(a, q, query_of(a, min(16, M) - 1));
   int t0 = from + wave * kStep;
@@ -820,7 +823,7 @@ __device__ __forceinline__ void weigh_stretch(const Kv8AttendArgs& a, const Requ
     for (int row0 = 16; row0 < M; row0 += 16) {
       RowTile<D> x;
       float z[4];
-      load_rows<D>(a, q, h, row0, g, m, x);
+      load_rows<D, false>(a, q, h, row0, g, m, x);
       row_lse(x.lse, row0 + m < M, g, z);
       add_weights<D, 2>(a, q, x.q, k, scale, z, row0 + 4 * g, false, t0 + m, acc);
     }
@@ -853,10 +856,11 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_weigh_pieces_kernel(Kv8Attend
 }
 
 // Many rows (prompts): the waves share 64 tokens, whose keys stay in registers,
-// and take row tiles in turn, the queries of the next ones in flight.
+// and take row tiles in turn, the queries of the next one in flight.  What the
+// loop reads over and over is the queries, so their pieces lie side by side.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2) kv8_weigh_rows_kernel(Kv8AttendArgs a) {
-  constexpr int SUB = 4, AHEAD = WA;     // row tiles in flight
+  constexpr int SUB = 4;
   __shared__ float red[kWaves][16 * SUB];
   const Kv8Cache& c = a.c;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -871,33 +875,50 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_weigh_rows_kernel(Kv8AttendAr
   float ks[SUB], acc[SUB];
 #pragma unroll
   for (int u = 0; u < SUB; ++u) {
-    u32x4 kw[D / 64];
     x[u] = tile_at(c, table, h, t0 + 16 * u, q.len);
-    load_k<D>(c, x[u], g, m, kw);
     ks[u] = c.k_scale[x[u].slab] * a.scale_log2;
-    convert_k<D>(kw, k[u]);
+    const uint8_t* p = c.k_pool + (x[u].slab * c.B + x[u].off) * D + m * D + 8 * g;
+#pragma unroll
+    for (int s = 0; s < D / 32; ++s) {
+      const u32x2 w = *(const u32x2*)(p + 32 * s);
+      k[u][s] = cvt8(w[0], w[1]);
+    }
     acc[u] = 0.0f;
   }
   const int M = q.n * a.G;
   // causal: the rows that see these tokens begin with those of query t0 - pos0
-  int row0 = 16 * wave;
-  if (a.causal && t0 > q.pos0) row0 += (int)min((int64_t)(t0 - q.pos0) * a.G / (16 * kWaves) * (16 * kWaves), (int64_t)M);
-  RowTile<D> rows[AHEAD];
-#pragma unroll
-  for (int b = 0; b < AHEAD - 1; ++b)
-    if (M > 0) load_rows<D>(a, q, h, row0 + b * 16 * kWaves, g, m, rows[b]);
-  for (; row0 < M; row0 += AHEAD * 16 * kWaves) {
-#pragma unroll
-    for (int b = 0; b < AHEAD; ++b) {
-      const int row = row0 + b * 16 * kWaves;
-      if (row >= M) break;
-      load_rows<D>(a, q, h, row + (AHEAD - 1) * 16 * kWaves, g, m, rows[(b + AHEAD - 1) % AHEAD]);
-      const Seen s_first = seen_by(a, q, query_of(a, row)), s_last = seen_by(a, q, query_of(a, min(row + 16, M) - 1));
-      if (s_last.hi <= t0 || s_first.lo >= t0 + 16 * SUB) continue;
-      const bool all = s_last.lo <= t0 && s_first.hi >= t0 + 16 * SUB;
-      float lse[4];
-      row_lse(rows[b].lse, row + m < M, g, lse);
-      add_weights<D, SUB>(a, q, rows[b].q, k, ks, lse, row + 4 * g, all, t0 + m, acc);
+  constexpr int kNext = 16 * kWaves;
+  int first = 0;
+  if (a.causal && t0 > q.pos0) first = (int)min((int64_t)(t0 - q.pos0) * a.G / kNext * kNext, (int64_t)M);
+  // The workgroups of a head read the same queries: each begins elsewhere, so
+  // that they do not all wait for the same lines to arrive from memory.
+  const int steps = (M - first + kNext - 1) / kNext;
+  int step = steps > 0 ? (int)(blockIdx.x * 5u % (unsigned)steps) : 0;
+  const auto turn = [&]() {
+    const int row = first + step * kNext + 16 * wave;
+    step = step + 1 == steps ? 0 : step + 1;
+    return row;
+  };
+  const auto add = [&](const RowTile<D>& x, int row) {
+    const Seen s_first = seen_by(a, q, query_of(a, min(row, M - 1)));
+    const Seen s_last = seen_by(a, q, query_of(a, min(row + 16, M) - 1));
+    if (row >= M || s_last.hi <= t0 || s_first.lo >= t0 + 16 * SUB) return;
+    float lse[4];
+    row_lse(x.lse, row + m < M, g, lse);
+    add_weights<D, SUB>(a, q, x.q, k, ks, lse, row + 4 * g, s_last.lo <= t0 && s_first.hi >= t0 + 16 * SUB, t0 + m, acc);
+  };
+  // two buffers by name: a copy of one would wait for its loads
+  RowTile<D> even, odd;
+  if (steps > 0) {
+    int row = turn();
+    load_rows<D, true>(a, q, h, row, g, m, even);
+    for (int n = 0; n < steps; n += 2) {
+      const int row1 = n + 1 < steps ? turn() : M;
+      load_rows<D, true>(a, q, h, row1, g, m, odd);
+      add(even, row);
+      row = n + 2 < steps ? turn() : M;
+      load_rows<D, true>(a, q, h, row, g, m, even);
+      add(odd, row1);
     }
   }
 #pragma unroll
