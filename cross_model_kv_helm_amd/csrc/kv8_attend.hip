@@ -855,13 +855,14 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_weigh_pieces_kernel(Kv8Attend
   weigh_stretch<D>(a, d.q, item, from, min(d.q.len, from + per));
 }
 
-// Many rows (prompts): the waves share 64 tokens, whose keys stay in registers,
+// Many rows (prompts): NW waves share 16*SUB tokens, whose keys stay in registers,
 // and take row tiles in turn, the queries of the next one in flight.  What the
-// loop reads over and over is the queries, so their pieces lie side by side.
-template <int D>
-__global__ void __launch_bounds__(kThreads, 2) kv8_weigh_rows_kernel(Kv8AttendArgs a) {
-  constexpr int SUB = 4;
-  __shared__ float red[kWaves][16 * SUB];
+// loop reads over and over is the queries: their pieces lie side by side, and
+// 128 tokens share a reading where there are workgroups enough (with 64 tokens
+// the queries came from L2 at 8 TB/s and bounded the kernel).
+template <int D, int SUB, int NW>
+__global__ void __launch_bounds__(64 * NW, 2) kv8_weigh_rows_kernel(Kv8AttendArgs a) {
+  __shared__ float red[NW][16 * SUB];
   const Kv8Cache& c = a.c;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
@@ -887,7 +888,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_weigh_rows_kernel(Kv8AttendAr
   }
   const int M = q.n * a.G;
   // causal: the rows that see these tokens begin with those of query t0 - pos0
-  constexpr int kNext = 16 * kWaves;
+  constexpr int kNext = 16 * NW;
   int first = 0;
   if (a.causal && t0 > q.pos0) first = (int)min((int64_t)(t0 - q.pos0) * a.G / kNext * kNext, (int64_t)M);
   // The workgroups of a head read the same queries: each begins elsewhere, so
@@ -925,16 +926,16 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_weigh_rows_kernel(Kv8AttendAr
   for (int u = 0; u < SUB; ++u) {
     acc[u] += __shfl_xor(acc[u], 16);
     acc[u] += __shfl_xor(acc[u], 32);
-    if (g == u) red[wave][lane] = acc[u];
+    if (g == 0) red[wave][16 * u + m] = acc[u];
   }
   __syncthreads();
-  if (wave == 0) {
-    float sum = red[0][lane];
+  const int tok = t0 + threadIdx.x;
+  if (threadIdx.x < 16 * SUB && tok < q.len) {
+    float sum = red[0][threadIdx.x];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) sum += red[w][lane];
-#pragma unroll
-    for (int u = 0; u < SUB; ++u)
-      if (g == u && x[u].ok && t0 + lane < q.len) a.weights[x[u].slab * c.B + x[u].off + m] += sum;
+    for (int w = 1; w < NW; ++w) sum += red[w][threadIdx.x];
+    const int blk = entry_at(c, table, tok, q.len), page = c.page_magic ? (int)__umulhi((uint32_t)tok >> 4, c.page_magic) : tok >> 4;
+    if ((uint32_t)blk < (uint32_t)c.n_blocks) a.weights[((int64_t)blk * c.H + h) * c.B + (tok - page * c.B)] += sum;
   }
 }
 
@@ -965,8 +966,13 @@ hipError_t attend(const Kv8AttendArgs& a, hipStream_t stream) {
 template <int D>
 hipError_t weigh(const Kv8AttendArgs& a, hipStream_t stream) {
   if (a.n_tok * a.G > 64 * (int64_t)a.c.R) {
-    const dim3 grid((unsigned)((a.c.max_len + 63) / 64), (unsigned)a.c.H, (unsigned)a.c.R);
-    kv8_weigh_rows_kernel<D><<<grid, kThreads, 0, stream>>>(a);
+    const auto grid = [&](int tokens) {
+      return dim3((unsigned)((a.c.max_len + tokens - 1) / tokens), (unsigned)a.c.H, (unsigned)a.c.R);
+    };
+    if ((int64_t)a.c.max_len * a.c.H * a.c.R >= 128 * 192)
+      kv8_weigh_rows_kernel<D, 8, 8><<<grid(128), 512, 0, stream>>>(a);
+    else
+      kv8_weigh_rows_kernel<D, 4, 4><<<grid(64), 256, 0, stream>>>(a);
   } else if (a.pieces) {
     kv8_weigh_pieces_kernel<D><<<dim3((unsigned)a.pieces), kThreads, 0, stream>>>(a);
   } else {
