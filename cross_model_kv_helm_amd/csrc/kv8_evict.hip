@@ -5,7 +5,7 @@
 // finds the key of the last token that stays and how many equal ones stay with
 // it, and each wave then writes the kept indices of its stretch of tokens,
 // ascending (the first of the equal ones, so ties go to the lowest index).
-// The keys are held in LDS where they fit (contexts up to 36,800 tokens), so
+// The keys are held in LDS where they fit (contexts up to 36,544 tokens), so
 // the weights are read once; else every pass reads them again.  Weights crowd
 // into few exponents: the histogram has 16 copies, one for every 16th lane, so
 // that at most four lanes meet in an atomic.
@@ -26,7 +26,7 @@ constexpr int kSelWaves = kSelThreads / 64;
 constexpr int kCopies = 16;
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kKeysInLds = 36800;        // with the histogram just under 160 KB
+constexpr int kKeysInLds = 36544;        // with the histogram just under 160 KB
 
 // Larger weight, larger key; -0 equals +0; NaN below -inf.
 __device__ __forceinline__ uint32_t key_of(float w) {
@@ -57,7 +57,7 @@ __device__ __forceinline__ u32x4 keys_at(const Kv8EvictArgs& a, const int32_t* r
 template <bool LDS>
 __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(Kv8EvictArgs a) {
   extern __shared__ uint32_t keys[];
-  __shared__ int hist[256 * kCopies];
+  __shared__ int hist[256 * kCopies], counts[256];
   __shared__ int found[2];                 // digit, how many of the tokens above stay
   __shared__ int above[kSelWaves], equal[kSelWaves];
   const Kv8Cache& c = a.c;
@@ -82,28 +82,42 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(Kv8EvictArgs a)
   }
   const auto four = [&](int t) { return LDS ? *(const u32x4*)&keys[t] : keys_at(a, row, h, t); };
 
+  for (int j = tid; j < 256 * kCopies; j += kSelThreads) hist[j] = 0;
+  __syncthreads();
   uint32_t prefix = 0, mask = 0;           // the digits found so far
   for (int shift = 24; need > 0 && shift >= 0; shift -= 8) {
-    for (int j = tid; j < 256 * kCopies; j += kSelThreads) hist[j] = 0;
-    __syncthreads();
+    int* mine = hist + (lane & (kCopies - 1));
     for (int t = 4 * tid; t < cand; t += 4 * kSelThreads) {
       const u32x4 k = four(t);
+      int digit = -1, run = 0;             // neighbours often share a digit: one atomic for a run of them
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (t + i < cand && (k[i] & mask) == prefix)
-          atomicAdd(&hist[((k[i] >> shift) & 255) * kCopies + (lane & (kCopies - 1))], 1);
+      for (int i = 0; i < 4; ++i) {
+        if (t + i >= cand || (k[i] & mask) != prefix) continue;
+        const int d = (k[i] >> shift) & 255;
+        if (d != digit) {
+          if (run) atomicAdd(&mine[digit * kCopies], run);
+          digit = d;
+          run = 0;
+        }
+        ++run;
+      }
+      if (run) atomicAdd(&mine[digit * kCopies], run);
     }
     __syncthreads();
     if (tid < 256) {
       int sum = 0;
 #pragma unroll
-      for (int j = 0; j < kCopies; ++j) sum += hist[tid * kCopies + ((j + tid) & (kCopies - 1))];
-      hist[tid * kCopies] = sum;           // a thread reads and writes its own digit's copies only
+      for (int j = 0; j < kCopies; ++j) {
+        int* x = &hist[tid * kCopies + ((j + tid) & (kCopies - 1))];
+        sum += *x;
+        *x = 0;                            // for the next digit
+      }
+      counts[tid] = sum;
     }
     __syncthreads();
     if (wave == 0) {   // from the largest digit down: lane l looks at digits 255-4l .. 252-4l
       int own = 0;
-      for (int j = 0; j < 4; ++j) own += hist[(255 - 4 * lane - j) * kCopies];
+      for (int j = 0; j < 4; ++j) own += counts[255 - 4 * lane - j];
       int before = own;
       for (int o = 1; o < 64; o <<= 1) {
         const int x = __shfl_up(before, o);
@@ -112,7 +126,7 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(Kv8EvictArgs a)
       before -= own;
       if (before < need && before + own >= need) {
         int d = 255 - 4 * lane;
-        while (before + hist[d * kCopies] < need) before += hist[d-- * kCopies];
+        while (before + counts[d] < need) before += counts[d--];
         found[0] = d;
         found[1] = before;
       }
@@ -121,7 +135,6 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(Kv8EvictArgs a)
     prefix |= (uint32_t)found[0] << shift;
     mask |= 255u << shift;
     need -= found[1];
-    __syncthreads();
   }
   // need: how many tokens of key `prefix` stay (0 only where none competes)
 
@@ -197,7 +210,7 @@ __global__ void __launch_bounds__(kThreads) kv8_copy_kernel(Kv8EvictArgs a) {
   const Kv8Cache& c = a.c;
   const int lane = threadIdx.x & 63;
   const int page = blockIdx.x * kWaves + (threadIdx.x >> 6), h = blockIdx.y, r = blockIdx.z;
-  const int keep = min(clamped_len(c, a.kv_len[r]), a.budget);
+  const int n = clamped_len(c, a.kv_len[r]), keep = min(n, a.budget);
   const int j0 = page * c.B;
   if (j0 >= keep) return;
   const int blk = a.dst[(int64_t)r * a.max_dst + page];
@@ -220,7 +233,7 @@ __global__ void __launch_bounds__(kThreads) kv8_copy_kernel(Kv8EvictArgs a) {
       from[i] = -1;
       off[i] = 0;
       if (u < all && j < cnt) {
-        const int t = kept[j], sp = page_of(c, t), sb = row[sp];
+        const int t = min((uint32_t)kept[j], (uint32_t)n - 1u), sp = page_of(c, t), sb = row[sp];
         off[i] = t - sp * c.B;
         if ((uint32_t)sb < (uint32_t)c.n_blocks) from[i] = (int64_t)sb * c.H + h;
       }

@@ -6,7 +6,8 @@
 // and once out and does 3 flops per value: it is bound by memory, and at a
 // few tokens by the launch.
 //
-// A workgroup takes a few tokens and a range of heads; the (cos, sin) of its
+// A workgroup takes a few tokens and a range of heads, those first that lie
+// side by side (a cache's tokens, a projection's heads); the (cos, sin) of its
 // tokens' pairs are formed once, in LDS, and serve all its heads.  The angle
 // is reduced in fp64, as turns = position * freq/(2 pi) less the nearest whole
 // number (positions up to 2^31 leave an error under 2e-7 rad), so that cos and
@@ -64,62 +65,90 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, RopeTurns f)
   const int h0 = blockIdx.y * a.heads_per;
   const int nh = min(a.heads_per, a.n_q + a.n_k - h0);
   const int turned = INTERLEAVED ? 2 * P / VEC : P / VEC;   // pieces that are turned
-  const int pieces = turned + (a.D - 2 * P + VEC - 1) / VEC;
-  const int total = nt * nh * pieces;
-  for (int e = threadIdx.x; e < total; e += kThreads) {
-    const int p = e % pieces, th = e / pieces;
-    const int h = h0 + th % nh, t = th / nh;
-    const bool is_q = h < a.n_q;
-    const int hh = is_q ? h : h - a.n_q;
-    const T* x = is_q ? (const T*)a.q + (t0 + t) * a.q_tok + hh * a.q_head
-                      : (const T*)a.k + (t0 + t) * a.k_tok + hh * a.k_head;
-    T* y = is_q ? (T*)a.out_q + (t0 + t) * a.oq_tok + hh * a.oq_head
-                : (T*)a.out_k + (t0 + t) * a.ok_tok + hh * a.ok_head;
-    if (p >= turned) {   // past the rotated part
-      const int d = 2 * P + (p - turned) * VEC;
-      if (d + VEC <= a.D) {
-        store_piece<T, VEC>(y + d, load_piece<T, VEC>(x + d));
+  const int total = nt * nh * a.pieces;
+  // A thread's pieces: all read, then turned, then written (an output may be
+  // its input, piece by piece).
+  constexpr int U = 4;
+  for (int e0 = threadIdx.x; e0 < total; e0 += U * kThreads) {
+    Piece<T, VEC> u[U], v[U];
+    T* y[U];
+    int p[U], t[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int e = e0 + i * kThreads;
+      p[i] = -1;
+      if (e >= total) continue;
+      const int th = (int)__umulhi((uint32_t)e, a.pieces_magic);
+      p[i] = e - th * a.pieces;
+      int h;
+      if (a.tokens_inner) {     // a head's tokens lie side by side
+        h = nt == 1 ? th : th / nt;
+        t[i] = th - h * nt;
       } else {
-        for (int j = d; j < a.D; ++j) y[j] = x[j];
+        t[i] = nh == 1 ? th : th / nh;
+        h = th - t[i] * nh;
       }
-    } else if constexpr (INTERLEAVED) {
-      auto v = load_piece<T, VEC>(x + p * VEC);
+      h += h0;
+      const bool is_q = h < a.n_q;
+      const int hh = is_q ? h : h - a.n_q;
+      const T* x = is_q ? (const T*)a.q + (t0 + t[i]) * a.q_tok + hh * a.q_head
+                        : (const T*)a.k + (t0 + t[i]) * a.k_tok + hh * a.k_head;
+      y[i] = is_q ? (T*)a.out_q + (t0 + t[i]) * a.oq_tok + hh * a.oq_head
+                  : (T*)a.out_k + (t0 + t[i]) * a.ok_tok + hh * a.ok_head;
+      const int d = p[i] < turned ? p[i] * VEC : 2 * P + (p[i] - turned) * VEC;
+      if (d + VEC <= a.D) {
+        u[i] = load_piece<T, VEC>(x + d);
+      } else {                  // the last values of a head that is no multiple of the piece
+        for (int j = d; j < a.D; ++j) y[i][j] = x[j];
+        p[i] = -1;
+        continue;
+      }
+      if (!INTERLEAVED && p[i] < turned) v[i] = load_piece<T, VEC>(x + P + d);
+    }
 #pragma unroll
-      for (int j = 0; j < VEC; j += 2) {
-        const float2 w = cs[t * P + (p * VEC + j) / 2];
-        const float u0 = to_f32<T>(v.v[j]), u1 = to_f32<T>(v.v[j + 1]);
-        v.v[j] = (T)(u0 * w.x - u1 * w.y);
-        v.v[j + 1] = (T)(u0 * w.y + u1 * w.x);
-      }
-      store_piece<T, VEC>(y + p * VEC, v);
-    } else {
-      auto u = load_piece<T, VEC>(x + p * VEC);
-      auto v = load_piece<T, VEC>(x + P + p * VEC);
+    for (int i = 0; i < U; ++i) {
+      if (p[i] < 0) continue;
+      if (p[i] >= turned) {     // past the rotated part
+        store_piece<T, VEC>(y[i] + 2 * P + (p[i] - turned) * VEC, u[i]);
+      } else if constexpr (INTERLEAVED) {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float2 w = cs[t * P + p * VEC + j];
-        const float u0 = to_f32<T>(u.v[j]), u1 = to_f32<T>(v.v[j]);
-        u.v[j] = (T)(u0 * w.x - u1 * w.y);
-        v.v[j] = (T)(u0 * w.y + u1 * w.x);
+        for (int j = 0; j < VEC; j += 2) {
+          const float2 w = cs[t[i] * P + (p[i] * VEC + j) / 2];
+          const float u0 = to_f32<T>(u[i].v[j]), u1 = to_f32<T>(u[i].v[j + 1]);
+          u[i].v[j] = (T)(u0 * w.x - u1 * w.y);
+          u[i].v[j + 1] = (T)(u0 * w.y + u1 * w.x);
+        }
+        store_piece<T, VEC>(y[i] + p[i] * VEC, u[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          const float2 w = cs[t[i] * P + p[i] * VEC + j];
+          const float u0 = to_f32<T>(u[i].v[j]), u1 = to_f32<T>(v[i].v[j]);
+          u[i].v[j] = (T)(u0 * w.x - u1 * w.y);
+          v[i].v[j] = (T)(u0 * w.y + u1 * w.x);
+        }
+        store_piece<T, VEC>(y[i] + p[i] * VEC, u[i]);
+        store_piece<T, VEC>(y[i] + P + p[i] * VEC, v[i]);
       }
-      store_piece<T, VEC>(y + p * VEC, u);
-      store_piece<T, VEC>(y + P + p * VEC, v);
     }
   }
 }
 
 template <typename T, int VEC, bool INTERLEAVED>
 hipError_t launch(RopeArgs a, const RopeTurns& f, hipStream_t stream) {
-  // About 16 pieces a thread at most, and enough workgroups for 256 CUs when
-  // there are few tokens: first one token and few heads, then more of both.
+  // Few tokens: a token and few heads a workgroup, for 256 CUs to have work.
+  // Many: up to 16 tokens and about 8 pieces a thread.
   const int heads = a.n_q + a.n_k;
-  const int pieces = (INTERLEAVED ? a.D : a.D / 2) / VEC + 1;
-  a.heads_per = heads;
+  a.pieces = (INTERLEAVED ? 2 * a.pairs / VEC : a.pairs / VEC) + (a.D - 2 * a.pairs + VEC - 1) / VEC;
+  // e / pieces = umulhi(e, magic) while e * pieces < 2^32: e is under 2^22 here, pieces at most 257
+  a.pieces_magic = (uint32_t)(((uint64_t(1) << 32) + a.pieces - 1) / a.pieces);
+  a.heads_per = heads < 1024 ? heads : 1024;
   a.tok = 1;
-  while (a.heads_per > 1 && a.heads_per * pieces > kThreads &&
+  while (a.heads_per > 1 && a.heads_per * a.pieces > kThreads &&
          a.n_tok * ((heads + a.heads_per - 1) / a.heads_per) < 1024)
     a.heads_per = (a.heads_per + 1) / 2;
-  while (a.tok < 16 && a.tok * heads * pieces < 4 * kThreads && a.n_tok / a.tok > 2048) a.tok *= 2;
+  while (a.tok < 16 && a.tok * a.heads_per * a.pieces < 8 * kThreads && a.n_tok / a.tok > 2048) a.tok *= 2;
+  a.tokens_inner = a.n_q ? a.q_head > a.q_tok : a.k_head > a.k_tok;
   const dim3 grid((unsigned)((a.n_tok + a.tok - 1) / a.tok), (unsigned)((heads + a.heads_per - 1) / a.heads_per));
   rope_kernel<T, VEC, INTERLEAVED><<<grid, kThreads, (size_t)a.tok * a.pairs * sizeof(float2), stream>>>(a, f);
   return hipGetLastError();

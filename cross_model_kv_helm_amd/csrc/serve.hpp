@@ -24,7 +24,9 @@ struct RopeArgs {
   int64_t q_tok, q_head, k_tok, k_head, oq_tok, oq_head, ok_tok, ok_head;   // element strides
   int32_t n_q, n_k, D, pairs;
   float mag, sign;           // what cos and sin are multiplied by; -1 turns back
-  int32_t tok, heads_per;    // set at the launch
+  // set at the launch: tokens and heads of a workgroup, pieces of a head
+  int32_t tok, heads_per, pieces, tokens_inner;
+  uint32_t pieces_magic;
 };
 hipError_t launch_rope(const RopeArgs& a, const RopeTurns& f, bool interleaved, Dtype dt, hipStream_t stream);
 
