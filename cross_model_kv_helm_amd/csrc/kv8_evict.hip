@@ -1,11 +1,12 @@
 // kv8_evict.hip — eviction by accumulated weight (helm_kv8_evict).
 //
 // Selection, one workgroup per (request, KV head): the weights become 32-bit
-// keys in the same order (NaN lowest), a radix selection of four 8-bit digits
-// finds the key of the last token that stays and how many equal ones stay with
-// it, and each wave then writes the kept indices of its stretch of tokens,
+// keys in the same order (NaN lowest), a radix selection by 8-bit digits finds
+// the key of the last token that stays and how many equal ones stay with it
+// (two digits leave few enough candidates, as a rule, for one wave to rank),
+// and each wave then writes the kept indices of its stretch of tokens,
 // ascending (the first of the equal ones, so ties go to the lowest index).
-// The keys are held in LDS where they fit (contexts up to 36,544 tokens), so
+// The keys are held in LDS where they fit (contexts up to 36,448 tokens), so
 // the weights are read once; else every pass reads them again.  Weights crowd
 // into few exponents: the histogram has 16 copies, one for every 16th lane, so
 // that at most four lanes meet in an atomic.
@@ -26,7 +27,7 @@ constexpr int kSelWaves = kSelThreads / 64;
 constexpr int kCopies = 16;
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kKeysInLds = 36544;        // with the histogram just under 160 KB
+constexpr int kKeysInLds = 36448;        // with the histogram just under 160 KB
 
 // Larger weight, larger key; -0 equals +0; NaN below -inf.
 __device__ __forceinline__ uint32_t key_of(float w) {
@@ -58,7 +59,9 @@ template <bool LDS>
 __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(Kv8EvictArgs a) {
   extern __shared__ uint32_t keys[];
   __shared__ int hist[256 * kCopies], counts[256];
-  __shared__ int found[2];                 // digit, how many of the tokens above stay
+  __shared__ int found[3];                 // digit, how many tokens lie above it, how many share it
+  __shared__ uint32_t few[64];
+  __shared__ int few_count;
   __shared__ int above[kSelWaves], equal[kSelWaves];
   const Kv8Cache& c = a.c;
   const int r = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
@@ -129,12 +132,41 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(Kv8EvictArgs a)
         while (before + counts[d] < need) before += counts[d--];
         found[0] = d;
         found[1] = before;
+        found[2] = counts[d];
       }
+      if (lane == 0) few_count = 0;
     }
     __syncthreads();
     prefix |= (uint32_t)found[0] << shift;
     mask |= 255u << shift;
     need -= found[1];
+    if (found[2] == need) break;           // every key that begins like this stays
+    if (found[2] > 64 || shift == 0) continue;
+    for (int t = 4 * tid; t < cand; t += 4 * kSelThreads) {
+      const u32x4 k = four(t);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (t + i < cand && (k[i] & mask) == prefix) few[atomicAdd(&few_count, 1)] = k[i];
+    }
+    __syncthreads();
+    if (wave == 0) {
+      const int some = __builtin_amdgcn_readfirstlane(found[2]);
+      const uint32_t mine = lane < some ? few[lane] : 0u;
+      int larger = 0, equals = 0;
+      for (int l = 0; l < some; ++l) {
+        const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)mine, l);
+        larger += other > mine;
+        equals += other == mine;
+      }
+      if (lane < some && larger < need && larger + equals >= need) {   // the same for all equal ones
+        found[0] = (int)mine;
+        found[1] = larger;
+      }
+    }
+    __syncthreads();
+    prefix = (uint32_t)found[0];
+    need -= found[1];
+    break;
   }
   // need: how many tokens of key `prefix` stay (0 only where none competes)
 

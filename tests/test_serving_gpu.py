@@ -256,7 +256,10 @@ CASES = [
     (16, 2, 4, 128, [1000, 37], [1, 1], True, 100),
     (16, 1, 2, 64, [513, 200], [150, 33], True, 7),
     (64, 1, 1, 128, [260], [260], True, 0),
-    (16, 8, 5, 128, [1500, 1], [300, 1], True, 0)]
+    (16, 8, 5, 128, [1500, 1], [300, 1], True, 0),
+    (16, 8, 2, 128, [3100, 700], [200, 90], True, 0),                  # enough tokens for the widest sharing
+    (32, 4, 1, 64, [6500], [70], True, 1000),
+    (16, 1, 3, 128, [9, 300, 0, 77] * 20, [1, 1, 0, 3] * 20, True, 0)]  # more requests than lanes
 
 
 def attend_inputs(B, H, G, D, kv, new, seed):
@@ -396,6 +399,36 @@ def test_evict(hk, B, H, D, kv, budget, recent):
     assert same_bits(w, weights)
     for n in ("k_scale", "v_scale", "k_pool", "v_pool"):
         assert same_bits(d[n], c[n]), n
+
+
+@pytest.mark.parametrize("n,budget,recent,spread", [
+    (40000, 3000, 100, "distinct"),          # more tokens than the selection holds in LDS
+    (9000, 4000, 0, "distinct"), (9000, 63, 10, "close"), (36448, 64, 0, "distinct"), (5000, 2500, 5, "signs"),
+    (4097, 1, 0, "equal"), (66, 65, 64, "distinct")])
+def test_evict_weights_of_every_spread(hk, n, budget, recent, spread):
+    B, H, D = 16, 1, 64
+    g = gen_of(n + budget)
+    c = ref.cache(g, [n], B, H, D, spare=-(-budget // B))
+    nb = c["k_pool"].shape[0]
+    used = set(c["table"][0].tolist())
+    dst = i32([[b for b in range(nb) if b not in used]])
+    weights = torch.rand((nb, H, B), generator=g)
+    if spread == "close":                    # keys that differ in their last digits only
+        weights = 1.0 + weights * 2.0 ** -18
+    elif spread == "signs":
+        weights = torch.randn((nb, H, B), generator=g) * torch.exp2(torch.randint(-140, 120, (nb, H, B), generator=g).float())
+    elif spread == "equal":
+        weights.fill_(0.25)
+    d = {k: t.cuda() for k, t in c.items()}
+    shape = hk.make_kv8_evict_shape(d["k_pool"], d["table"], dst, budget, recent, max_kv_len=n)
+    w = weights.cuda()
+    kept, _ = hk.helm_kv8_evict(w, i32([n]).cuda(), d["table"], dst.cuda(), d["k_pool"], d["v_pool"], d["k_scale"],
+                                d["v_scale"], shape)
+    want, _ = ref.evict(weights, [n], c["table"], dst, c["k_pool"], c["v_pool"], c["k_scale"], c["v_scale"], budget,
+                        recent, n)
+    assert torch.equal(kept.cpu(), want) and same_bits(w, weights)
+    for x in ("k_scale", "v_scale", "k_pool", "v_pool"):
+        assert same_bits(d[x], c[x]), x
 
 
 def test_evict_absent_pages_go_first(hk):
