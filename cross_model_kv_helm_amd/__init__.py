@@ -606,6 +606,17 @@ def _serving_shape(shape, t):
     return s
 
 
+def _new(shape, dtype, like, stream):
+    """An output or workspace for a launch on ``stream`` (0: torch's current
+    one), allocated on that stream: it is not handed on before the stream's
+    work is done, and what held it before was done on that stream too."""
+    import torch
+    if not stream or stream == _stream_of(like):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=like.device)):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
 def make_rope(head_dim: int, theta: float, rot_dim: int = None, layout: int = HELM_ROPE_HALF,
               scaling: int = HELM_ROPE_PLAIN, factor: float = 1.0, original_len: float = 0.0,
               beta_fast: float = 32.0, beta_slow: float = 1.0, low_freq: float = 1.0, high_freq: float = 4.0,
@@ -719,13 +730,12 @@ def helm_kv8_attend(q, cu_seqlens, kv_len, block_table, k_pool, v_pool, k_scale,
     nhd = (s.n_tokens, s.n_q_heads, s.head_dim)
     qp, s.tok_stride, s.head_stride = _heads_ptr(q, "q", torch.bfloat16, nhd)
     if out is None:
-        out = torch.empty(nhd, dtype=torch.bfloat16, device=q.device)
+        out = _new(nhd, torch.bfloat16, q, shape.stream)
     if lse is None:
-        lse = torch.empty(nhd[:2], dtype=torch.float32, device=q.device)
+        lse = _new(nhd[:2], torch.float32, q, shape.stream)
     if workspace is None:
         n = helm_kv8_attend_workspace_bytes(s)
-        workspace = (torch.empty(n, dtype=torch.uint8, device=q.device) if not shape.stream
-                     else _own_workspace(n, q.device, s.stream))
+        workspace = _new((n,), torch.uint8, q, shape.stream)
         s.workspace, s.workspace_bytes = workspace.data_ptr(), n
     else:
         s.workspace, s.workspace_bytes = _workspace_ptr(workspace, q.device)
@@ -769,9 +779,9 @@ def helm_kv8_evict(weights, kv_len, src_block_table, dst_block_table, k_pool, v_
     s = _serving_shape(shape, k_pool)
     R, H = s.n_requests, s.n_kv_heads
     if kept is None:
-        kept = torch.empty((R, H, s.budget), dtype=torch.int32, device=k_pool.device)
+        kept = _new((R, H, s.budget), torch.int32, k_pool, shape.stream)
     if new_len is None:
-        new_len = torch.empty((R,), dtype=torch.int32, device=k_pool.device)
+        new_len = _new((R,), torch.int32, k_pool, shape.stream)
     _raise(lib().helm_kv8_evict(_ptr(kv_len, "kv_len", torch.int32, (R,)),
                                 _ptr(src_block_table, "src_block_table", torch.int32, (R, s.max_blocks_src)),
                                 _ptr(dst_block_table, "dst_block_table", torch.int32, (R, s.max_blocks_dst)),

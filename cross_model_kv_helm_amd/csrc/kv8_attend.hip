@@ -15,7 +15,8 @@
 //   - codes d = m*D/16.. of tokens 4g..4g+3 of two tiles for O^T, whose 4x4
 //     byte blocks it transposes in registers (v_perm): output row m of the
 //     j-th product is d = m*D/16 + j.
-// Both loads cover whole 128-byte tokens; nothing is staged in LDS.
+// Both loads cover whole 128-byte tokens; keys and values are not staged in
+// LDS.
 //
 // The softmax runs over the tokens in one pass: per query row a reference
 // mref (a recent maximum), l = sum 2^(x - mref) and O, with x in units of
@@ -25,6 +26,14 @@
 //
 // A row of the products is a (query, head of the group) pair: single tokens of
 // a group of up to 16 heads share each key read.
+//
+// Bounds and what was measured (one MI355X, 8 KV heads of 128): decode reads
+// 256 bytes a token and head and is bound by memory, 32 ragged requests of 273 K
+// tokens in 117 us with the join (4.7 TB/s), one of 131,072 tokens in 61 us.
+// Prompts are bound by issue: a 64 x 32 step of a wave is 1,024 cycles of
+// matrix work beside 1,600 of vector work (the codes' conversion, the softmax),
+// which overlap between two waves only in part; two requests of up to 2,048
+// tokens over 8,192, 40 query heads: 402 us, 857 TFLOP/s.
 #include <math.h>
 
 #include "serve.hpp"
@@ -32,15 +41,6 @@
 namespace helm {
 namespace {
 
-#ifndef PT
-#define PT 128
-#endif
-#ifndef WFILL
-#define WFILL 768
-#endif
-#ifndef FILL
-#define FILL 768
-#endif
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -301,14 +301,18 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
   const int row0 = st.tile * TR, rowg = row0 + 16 * MT * rg;      // the workgroup's, this wave's
   const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
 
-  constexpr bool QL = MT > 2;
-  bf16x8 qv[QL ? 1 : MT][KS];
+  // Wide row tiles fill the registers with O: their queries wait in LDS, the
+  // scheduler is kept from mixing the phases of a step (let loose it spilled 47
+  // registers, 748 us where this takes 437), and a wave in its matrix phases
+  // goes before one in its softmax (402 us).
+  constexpr bool kWide = MT > 2;
+  bf16x8 qv[kWide ? 1 : MT][KS];
   Seen see[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
     const int row = min(rowg + 16 * t + m, M - 1);
     see[t] = seen_by(a, q, query_of(a, row));
-    if constexpr (QL) {
+    if constexpr (kWide) {
       if (t / (MT / TG) == tg) {
         bf16x8 v[KS];
         load_q<D>(a, q, h, row, g, v);
@@ -319,7 +323,7 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
       load_q<D>(a, q, h, row, g, qv[t]);
     }
   }
-  if constexpr (QL) __syncthreads();
+  if constexpr (kWide) __syncthreads();
   const int last = min(rowg + 16 * MT, M) - 1;
   const Seen s_first = seen_by(a, q, min(rowg, M - 1) / a.G), s_last = seen_by(a, q, last / a.G);
   // a wave of a row group that has no rows left (rowg >= M) finds begin >= end
@@ -363,7 +367,7 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
 
   for (; t0 < end; t0 += kStride) {
     f32x4 s[MT][2];
-    if constexpr (QL) __builtin_amdgcn_s_setprio(1);
+    if constexpr (kWide) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int t = 0; t < MT; ++t) s[t][0] = s[t][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -374,13 +378,16 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         bf16x8 qq;
-        if constexpr (QL) qq = __builtin_bit_cast(bf16x8, lds.q[((rg * MT + t) * KS + i) * 64 + lane]); else qq = qv[t][i];
+        if constexpr (kWide)
+          qq = __builtin_bit_cast(bf16x8, lds.q[((rg * MT + t) * KS + i) * 64 + lane]);
+        else
+          qq = qv[t][i];
         s[t][0] = mfma(k[0], qq, s[t][0]);
         s[t][1] = mfma(k[1], qq, s[t][1]);
       }
-      if constexpr (QL) __builtin_amdgcn_sched_barrier(0x100);
+      if constexpr (kWide) __builtin_amdgcn_sched_barrier(0x100);
     }
-    if constexpr (QL) __builtin_amdgcn_s_setprio(0);
+    if constexpr (kWide) __builtin_amdgcn_s_setprio(0);
     fetch_k(t0 + kStride, next);
 
     float lv[2], inv[2];
@@ -427,9 +434,9 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       pv[t] = probabilities<D>(s[t], now.ks, lv, inv, mref[t], l[t], o[t]);
-      if constexpr (QL) __builtin_amdgcn_sched_barrier(0x100);
+      if constexpr (kWide) __builtin_amdgcn_sched_barrier(0x100);
     }
-    if constexpr (QL) __builtin_amdgcn_s_setprio(1);
+    if constexpr (kWide) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int b = 0; b < D / 64; ++b) {
       uint32_t w0[4], w1[4];
@@ -444,7 +451,7 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u) load_v<D>(c, next.x[u], g, m, w.v[u]);
-    if constexpr (QL) __builtin_amdgcn_s_setprio(0);
+    if constexpr (kWide) __builtin_amdgcn_s_setprio(0);
     now = next;
   }
 
@@ -473,7 +480,7 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
         write_row<D>(a, row_at(rowg + 16 * t + m), st.piece, rowg - row0 + 16 * t + m, g, mref[t], l[t], o[t]);
   } else if constexpr (TG == 2) {   // each of the two finishes half of the row tiles
     constexpr int HT = MT / 2;
-    if constexpr (QL) __syncthreads();
+    if constexpr (kWide) __syncthreads();   // the queries' room is reused
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       if (g == 0) {
@@ -934,7 +941,8 @@ __global__ void __launch_bounds__(64 * NW, 2) kv8_weigh_rows_kernel(Kv8AttendArg
     float sum = red[0][threadIdx.x];
 #pragma unroll
     for (int w = 1; w < NW; ++w) sum += red[w][threadIdx.x];
-    const int blk = entry_at(c, table, tok, q.len), page = c.page_magic ? (int)__umulhi((uint32_t)tok >> 4, c.page_magic) : tok >> 4;
+    const int blk = entry_at(c, table, tok, q.len);
+    const int page = c.page_magic ? (int)__umulhi((uint32_t)tok >> 4, c.page_magic) : tok >> 4;
     if ((uint32_t)blk < (uint32_t)c.n_blocks) a.weights[((int64_t)blk * c.H + h) * c.B + (tok - page * c.B)] += sum;
   }
 }
@@ -943,11 +951,14 @@ template <int D>
 hipError_t attend(const Kv8AttendArgs& a, hipStream_t stream) {
   if (a.pieces == 0) {
     const dim3 grid((unsigned)(a.tiles * a.c.H));
-    if (a.row_tile == 128)
-      kv8_attend_kernel<D, 4, 2><<<grid, kThreads, 0, stream>>>(a);
-    else if (a.row_tile == 64)
-      kv8_attend_kernel<D, 2, 2><<<grid, kThreads, 0, stream>>>(a);
-    else if (a.row_tile == 32)
+    if constexpr (D == 128) {
+      if (a.row_tile == 128)
+        kv8_attend_kernel<D, 4, 2><<<grid, kThreads, 0, stream>>>(a);
+      else if (a.row_tile == 64)
+        kv8_attend_kernel<D, 2, 2><<<grid, kThreads, 0, stream>>>(a);
+      if (a.row_tile >= 64) return hipGetLastError();
+    }
+    if (a.row_tile == 32)
       kv8_attend_kernel<D, 2, 1><<<grid, kThreads, 0, stream>>>(a);
     else
       kv8_attend_kernel<D, 1, 1><<<grid, kThreads, 0, stream>>>(a);
@@ -983,6 +994,11 @@ hipError_t weigh(const Kv8AttendArgs& a, hipStream_t stream) {
 
 }  // namespace
 
+// Three workgroups a CU are resident with 16 rows (two with 32).  One round of
+// equal pieces beat both fewer and more: 32 ragged requests 117 us with 768,
+// 144 with 512, 129 with 1,536; a 131,072-token context 61, 63 and 67 us.
+constexpr int64_t kFill = 768;
+
 // Pieces for `items` items (at most `most`), in whose contexts the queries see
 // `span` tokens at most; `fill` workgroups fill the chip once.
 static void divide(Kv8AttendArgs& a, int64_t items, int64_t most, int64_t fill) {
@@ -1003,15 +1019,22 @@ void kv8_attend_plan(Kv8AttendArgs& a) {
   a.row_tile = rows <= 16 * R ? 16 : 32;
   const int64_t some = R < a.n_tok ? R : a.n_tok;      // requests with queries, at most
   const int64_t full = (rows + a.row_tile - 1) / a.row_tile, most = rows / a.row_tile + R;
-  divide(a, (full < some ? some : full) * a.c.H, (most < rows ? most : rows) * a.c.H, a.row_tile == 16 ? FILL : FILL * 2 / 3);
-  if (a.pieces == 0 && a.row_tile == 32 && rows > 48 * R) a.row_tile = PT;
+  divide(a, (full < some ? some : full) * a.c.H, (most < rows ? most : rows) * a.c.H, a.row_tile == 16 ? kFill : kFill * 2 / 3);
+  // Whole contexts: larger tiles share each reading and conversion of a context
+  // among more rows, where a request has the rows and the chip the workgroups.
+  // D = 128, us with 32 / 64 / 128 rows: 64 requests of 80 rows over 2,048
+  // tokens 108 / 107 / 127, 64 of 120 rows 129 / 118 / 137, 32 of 200 rows
+  // 117 / 110 / 84, 8 of 1,000 rows 110 / 100 / 78.  D = 64 (fewer registers
+  // a row, more waves): 54 / 63 / 78, 70 / 71 / 82, 59 / 63 / 77, 64 / 63 / 76.
+  if (a.pieces == 0 && a.row_tile == 32 && a.c.D == 128)
+    a.row_tile = rows > 160 * R && rows / 128 * a.c.H >= 512 ? 128 : rows > 48 * R ? 64 : 32;
   a.tiles = rows / a.row_tile + R;
 }
 
 void kv8_weigh_plan(Kv8AttendArgs& a) {
   const int64_t some = a.c.R < a.n_tok ? a.c.R : a.n_tok;
   a.row_tile = 0x7fffffff;     // an item has all rows of a request and head
-  divide(a, some * a.c.H, some * a.c.H, WFILL);
+  divide(a, some * a.c.H, some * a.c.H, kFill);
 }
 
 size_t kv8_attend_workspace(const Kv8AttendArgs& a) {

@@ -127,20 +127,23 @@ __device__ __forceinline__ int64_t cu_at(const int32_t* cu, int r, int64_t n_tok
 // A ragged batch is given work items without the host reading its lengths:
 // request r owns the items from base(r) = floor(cu[r] * num / den) + slack * r
 // up to base(r + 1), at least floor(n * num / den) + slack of them.  Returns
-// the owner of `item` and sets its base.  Uniform over the wave.
+// the owner of `item` and sets its base.  Uniform over the wave, which looks
+// at 64 requests at a time (of many requests at every 64th part first).
 __device__ __forceinline__ int owner_of(const int32_t* cu, int R, int64_t n_tok, int num, int den, int slack,
                                         int64_t item, int64_t& base) {
   const int lane = threadIdx.x & 63;
-  int count = 0;
-  for (int r0 = 0; r0 < R; r0 += 64) {
-    const int r = r0 + lane;
-    const bool under = r < R && cu_at(cu, r, n_tok) * num / den + (int64_t)slack * r <= item;
-    const int c = __popcll(__ballot(under));
-    count += c;
-    if (c < 64) break;
+  const auto base_of = [&](int r) { return cu_at(cu, r, n_tok) * num / den + (int64_t)slack * r; };
+  int lo = 0, size = R;
+  for (;;) {
+    const int step = (size + 63) / 64;
+    const bool under = lane * step < size && base_of(lo + lane * step) <= item;
+    const int k = max(__popcll(__ballot(under)) - 1, 0);
+    lo += k * step;
+    if (step == 1) break;
+    size = min(step, size - k * step);
   }
-  const int r = __builtin_amdgcn_readfirstlane(max(count - 1, 0));
-  base = cu_at(cu, r, n_tok) * num / den + (int64_t)slack * r;
+  const int r = __builtin_amdgcn_readfirstlane(lo);
+  base = base_of(r);
   return r;
 }
 
