@@ -612,9 +612,9 @@ def _new(shape, dtype, like, stream):
     work is done, and what held it before was done on that stream too."""
     import torch
     if not stream or stream == _stream_of(like):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=like.device)):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def make_rope(head_dim: int, theta: float, rot_dim: int = None, layout: int = HELM_ROPE_HALF,

@@ -243,12 +243,22 @@ struct Stretch {
   int64_t piece;     // < 0: the whole context, results are final; else where its sums go
 };
 // The workspace: per piece the (m, l) of its rows, behind them all the D sums
-// of each row.
+// of each row, and behind those what each piece is of (for the join, which
+// would take 3 us to work it out again).
 __device__ __forceinline__ float* piece_ml(const Kv8AttendArgs& a, int64_t piece, int row) {
   return a.part + (piece * a.row_tile + row) * 2;
 }
 __device__ __forceinline__ float* piece_sums(const Kv8AttendArgs& a, int64_t piece, int row) {
   return a.part + (int64_t)a.pieces * a.row_tile * 2 + (piece * a.row_tile + row) * a.c.D;
+}
+
+struct PieceOf {
+  int first, pieces, part;   // the item's first piece, how many it has (0: no such piece), which this is
+  int row0, rows, h, q0;     // its first row and rows, its KV head, packed index of the request's first query
+  int unused;
+};
+__device__ __forceinline__ PieceOf* piece_of(const Kv8AttendArgs& a, int64_t piece) {
+  return (PieceOf*)(a.part + (int64_t)a.pieces * a.row_tile * (2 + a.c.D)) + piece;
 }
 
 // A row of an item, D/16 values a lane and i: final, or one piece's.
@@ -638,10 +648,14 @@ __device__ __forceinline__ bool division_at(const Kv8AttendArgs& a, int key, Div
 template <int D, int MT>
 __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) kv8_attend_pieces_kernel(Kv8AttendArgs a) {
   __shared__ AttendLds<D, MT, 1> lds;
-  Division d;
-  if (!division_at(a, blockIdx.x, d)) return;
-  const int in = (int)blockIdx.x - d.first, item = in / d.pieces, part = in - item * d.pieces;
-  if (item >= d.items) return;
+  Division d = {};
+  bool mine = division_at(a, blockIdx.x, d);
+  const int in = (int)blockIdx.x - d.first, item = mine ? in / d.pieces : 0, part = mine ? in - item * d.pieces : 0;
+  mine = mine && item < d.items;
+  if (!mine) {
+    if (threadIdx.x == 0) piece_of(a, blockIdx.x)->pieces = 0;
+    return;
+  }
   const int per = (d.units + d.pieces - 1) / d.pieces * kUnit;
   Stretch st;
   st.tile = item / a.c.H;
@@ -650,6 +664,12 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) kv8_attend_pieces_k
   st.to = min(d.q.len, st.from + per);
   st.piece = d.pieces == 1 ? -1 : (int64_t)blockIdx.x;
   attend_stretch<D, MT, 1>(a, d.q, st, lds);
+  // last: behind a store the compiler no longer reads the tables through the scalar cache
+  if (threadIdx.x == 0) {
+    const int row0 = st.tile * a.row_tile;
+    *piece_of(a, blockIdx.x) = PieceOf{(int)blockIdx.x - part, d.pieces, part, row0,
+                                       min(a.row_tile, d.q.n * a.G - row0), st.h, (int)d.q.c0, 0};
+  }
 }
 
 // Joins the pieces of the items that were cut: the workgroup of a piece takes
@@ -660,15 +680,11 @@ __global__ void __launch_bounds__(kThreads) kv8_join_kernel(Kv8AttendArgs a) {
   constexpr int NG = kThreads * 4 / D;
   __shared__ float red_m[kWaves], red_l[NG];
   __shared__ f32x4 red_o[NG][D / 4];
-  Division x;
-  if (!division_at(a, blockIdx.x, x) || x.pieces == 1) return;
-  const int in = (int)blockIdx.x - x.first, item = in / x.pieces, part = in - item * x.pieces;
-  if (item >= x.items) return;
-  const int tile = item / a.c.H, h = item - tile * a.c.H;
-  const int64_t first = blockIdx.x - part;
-  const int rows = min(a.row_tile, x.q.n * a.G - tile * a.row_tile);
+  const PieceOf x = *piece_of(a, blockIdx.x);
+  if (x.pieces <= 1) return;           // no piece, or a whole context
+  const int64_t first = x.first;
   const int d = threadIdx.x % (D / 4), grp = threadIdx.x / (D / 4);
-  for (int row = part; row < rows; row += x.pieces) {
+  for (int row = x.part; row < x.rows; row += x.pieces) {
     float top = -3.402823466e38f;
     for (int s = threadIdx.x; s < x.pieces; s += kThreads) top = fmaxf(top, piece_ml(a, first + s, row)[0]);
 #pragma unroll
@@ -697,8 +713,8 @@ __global__ void __launch_bounds__(kThreads) kv8_join_kernel(Kv8AttendArgs a) {
         v += red_o[i][d];
       }
       v *= sum == 0.0f ? 0.0f : 1.0f / sum;
-      const int full = tile * a.row_tile + row;
-      const int64_t at = (x.q.c0 + full / a.G) * a.Hq + h * a.G + full % a.G;
+      const int i = query_of(a, x.row0 + row);
+      const int64_t at = (int64_t)(x.q0 + i) * a.Hq + x.h * a.G + (x.row0 + row - i * a.G);
       const bf16x2 lo = {(__bf16)v[0], (__bf16)v[1]}, hi = {(__bf16)v[2], (__bf16)v[3]};
       *(u32x2*)(a.out + at * D + 4 * d) = u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
       if (d == 0) a.lse[at] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
@@ -1038,7 +1054,7 @@ void kv8_weigh_plan(Kv8AttendArgs& a) {
 }
 
 size_t kv8_attend_workspace(const Kv8AttendArgs& a) {
-  return (size_t)a.pieces * a.row_tile * (2 + a.c.D) * sizeof(float);
+  return (size_t)a.pieces * (a.row_tile * (2 + a.c.D) * sizeof(float) + sizeof(PieceOf));
 }
 
 hipError_t launch_kv8_attend(const Kv8AttendArgs& a, hipStream_t stream) {
