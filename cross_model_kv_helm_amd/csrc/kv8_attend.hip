@@ -45,6 +45,7 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kTiny = 1.17549435e-38f;   // the smallest normal number
 constexpr float kLazy = 8.0f;       // log2 of how far sums may outgrow mref
 constexpr int kStep = 32;           // tokens a wave takes at a time: the second product's depth
 
@@ -116,8 +117,8 @@ __device__ __forceinline__ Tile tile_at(const Kv8Cache& c, const int32_t* row, i
 }
 
 // Keys of a tile: this lane's D/4 codes, 64 consecutive ones of a token by the
-// four lanes that share it (pieces 32 apart took twice the cache accesses).  (A uniform base and a 32-bit lane
-// offset: one address register.)
+// four lanes that share it.  (A uniform base and a 32-bit lane offset: one
+// address register.)
 template <int D>
 __device__ __forceinline__ void load_k(const Kv8Cache& c, const Tile& x, int g, int m, u32x4 (&w)[D / 64]) {
   const uint8_t* p = c.k_pool + (x.slab * c.B + x.off) * D;
@@ -139,17 +140,6 @@ __device__ __forceinline__ void load_q(const Kv8AttendArgs& a, const Request& q,
   const uint16_t* p = a.q + (q.c0 + i) * a.q_tok + (int64_t)(h * a.G + row - i * a.G) * a.q_head + g * 16;
 #pragma unroll
   for (int s = 0; s < D / 32; ++s) __builtin_memcpy(&v[s], p + 64 * (s >> 1) + 8 * (s & 1), 16);
-}
-
-template <int D>
-__device__ __forceinline__ f32x4 scores(const u32x4 (&k)[D / 64], const bf16x8 (&q)[D / 32]) {
-  f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int i = 0; i < D / 64; ++i) {
-    s = mfma(cvt8(k[i][0], k[i][1]), q[2 * i], s);
-    s = mfma(cvt8(k[i][2], k[i][3]), q[2 * i + 1], s);
-  }
-  return s;
 }
 
 // Tokens [lo, hi) that a query row sees.
@@ -261,20 +251,10 @@ __device__ __forceinline__ PieceOf* piece_of(const Kv8AttendArgs& a, int64_t pie
   return (PieceOf*)(a.part + (int64_t)a.pieces * a.row_tile * (2 + a.c.D)) + piece;
 }
 
-// A row of an item, D/16 values a lane and i: final, or one piece's.
+// A row's result, D/16 values a lane and i.
 template <int D>
-__device__ __forceinline__ void write_row(const Kv8AttendArgs& a, int64_t at, int64_t piece, int row, int g, float top,
-                                          float sum, const f32x4 (&o)[D / 16]) {
-  if (piece >= 0) {
-    if (g == 0) *(f32x2*)piece_ml(a, piece, row) = f32x2{top, sum};
-    float* v = piece_sums(a, piece, row) + g * (D / 4);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int b = 0; b < D / 64; ++b)
-        *(f32x4*)(v + (D / 16) * i + 4 * b) = f32x4{o[4 * b][i], o[4 * b + 1][i], o[4 * b + 2][i], o[4 * b + 3][i]};
-    return;
-  }
+__device__ __forceinline__ void write_row(const Kv8AttendArgs& a, int64_t at, int g, float top, float sum,
+                                          const f32x4 (&o)[D / 16]) {
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // a row that sees nothing: 0
   uint16_t* y = a.out + at * D + g * (D / 4);
 #pragma unroll
@@ -291,7 +271,8 @@ __device__ __forceinline__ void write_row(const Kv8AttendArgs& a, int64_t at, in
 template <int D, int MT, int RG>
 struct AttendLds {
   static constexpr int TG = kWaves / RG, PAD = D + 4;
-  static constexpr int kJoinRows = TG == 4 ? 16 * MT : TG == 2 ? 8 * MT : 1;   // of a wave, exchanged at the end
+  static_assert(TG == 4 || TG == 2);
+  static constexpr int kJoinRows = TG == 4 ? 16 * MT : 8 * MT;   // of a wave, exchanged at the end
   union {
     float o[kWaves][kJoinRows][PAD];
     u32x4 q[MT > 2 ? RG * MT * (D / 32) * 64 : 1];
@@ -405,13 +386,13 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       there = there && now.x[u].ok;
-      odd = odd || !now.x[u].ok || !(now.vs[u] > 0.0f);
+      odd = odd || !now.x[u].ok || !(now.vs[u] >= kTiny);
     }
     // tokens past the context are not read as numbers: their codes may be anything
     if (odd) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const bool none = !now.x[u].ok || !(now.vs[u] > 0.0f);
+        const bool none = !now.x[u].ok || !(now.vs[u] >= kTiny);     // no scale: values of 0
         if (none) now.vs[u] = 1.0f;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -423,7 +404,7 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      now.ks[u] = fmaxf(now.ks[u] * a.scale_log2, 1.17549435e-38f);
+      now.ks[u] = fmaxf(now.ks[u] * a.scale_log2, kTiny);
       lv[u] = __builtin_amdgcn_logf(now.vs[u]);
       inv[u] = __builtin_amdgcn_rcpf(now.vs[u]);
     }
@@ -483,12 +464,7 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
         *(f32x4*)&lds.o[wave][16 * slot + m][g * (D / 4) + (D / 16) * i + 4 * b] =
             f32x4{o[t][4 * b][i], o[t][4 * b + 1][i], o[t][4 * b + 2][i], o[t][4 * b + 3][i]};
   };
-  if constexpr (TG == 1) {
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-      if (rowg + 16 * t + m < M) 
-        write_row<D>(a, row_at(rowg + 16 * t + m), st.piece, rowg - row0 + 16 * t + m, g, mref[t], l[t], o[t]);
-  } else if constexpr (TG == 2) {   // each of the two finishes half of the row tiles
+  if constexpr (TG == 2) {          // each of the two finishes half of the row tiles
     constexpr int HT = MT / 2;
     if constexpr (kWide) __syncthreads();   // the queries' room is reused
 #pragma unroll
@@ -515,9 +491,9 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
 #pragma unroll
           for (int j = 0; j < 4; ++j) o[t][4 * b + j][i] = f * o[t][4 * b + j][i] + fo * v[j];
         }
-      write_row<D>(a, row_at(row), st.piece, row - row0, g, top, f * l[t] + fo * lds.l[other][16 * t + m], o[t]);
+      write_row<D>(a, row_at(row), g, top, f * l[t] + fo * lds.l[other][16 * t + m], o[t]);
     }
-  } else {                          // few rows: all threads side by side over them
+  } else {                          // few rows, of a whole context or a piece: all threads side by side
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       if (g == 0) {
