@@ -1,11 +1,11 @@
 // kv8_attend.hip — attention over the 8-bit paged cache (helm_kv8_attend) and
 // the weight it gives each cached token (helm_kv8_weigh).
 //
-// Matrix products are v_mfma_f32_16x16x32_bf16 with both codes taken to bf16
-// (exact: e4m3 has fewer bits) and q as it is; a block's scale multiplies the
-// scores of its tokens (K) and, as log2 added to the exponent, their
-// probabilities (V) instead of the codes: a token far below the maximum whose
-// values are large does not underflow on the way.
+// The first product is v_mfma_f32_16x16x32_bf16 with the codes taken to bf16
+// (exact: e4m3 has fewer bits) and q as it is, the second the f16 form with the
+// codes taken to f16 (exact too) and p rounded to f16.  A block's scale
+// multiplies the scores of its tokens (K) and, as log2 added to the exponent,
+// their probabilities (V) instead of the codes.
 // Scores are formed transposed, S^T = K Q^T: in the result a lane holds four
 // tokens of one query row, which is where the second product, O^T = V^T P^T,
 // takes its right operand from — P never leaves the registers.  The order of
@@ -19,10 +19,13 @@
 // LDS.
 //
 // The softmax runs over the tokens in one pass: per query row a reference
-// mref (a recent maximum), l = sum 2^(x - mref) and O, with x in units of
-// log2.  A wave rescales only where some x exceeds its row's mref by more than
-// 8: sums then hold values up to 2^8 times larger, which costs fp32 and bf16
-// no precision, and the steady state has no exchange between lanes.
+// mref, l = sum p / (value scale) and O, with p = 2^(x - mref) and x the score
+// in units of log2 plus log2 of the value scale.  mref is set 7 below a maximum
+// and moves, rescaling l and O, only where some x exceeds it by more than 15:
+// the steady state has no exchange between lanes, p stays below f16's largest
+// number, and what lies 2^-32 below a row's largest p still counts.  p is
+// rounded to f16, half a step of 2^-11: with bf16 the error against fp64 of rows
+// that few tokens share was 1.4 times that of the rounded result itself.
 //
 // A row of the products is a (query, head of the group) pair: single tokens of
 // a group of up to 16 heads share each key read.
@@ -46,7 +49,8 @@ constexpr int kWaves = kThreads / 64;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTiny = 1.17549435e-38f;   // the smallest normal number
-constexpr float kLazy = 8.0f;       // log2 of how far sums may outgrow mref
+// log2 of a row's largest p: after mref was set, and at most
+constexpr float kFresh = 7.0f, kMost = 15.0f;
 constexpr int kStep = 32;           // tokens a wave takes at a time: the second product's depth
 
 __device__ __forceinline__ bf16x2 cvt_pair(uint32_t w, bool high) {
@@ -57,6 +61,16 @@ __device__ __forceinline__ bf16x2 cvt_pair(uint32_t w, bool high) {
 __device__ __forceinline__ bf16x8 cvt8(uint32_t lo, uint32_t hi) {
   const bf16x2 a = cvt_pair(lo, false), b = cvt_pair(lo, true), c = cvt_pair(hi, false), d = cvt_pair(hi, true);
   return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ f16x8 cvt8_f16(uint32_t lo, uint32_t hi) {
+  const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)lo, 1.0f, false);
+  const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)lo, 1.0f, true);
+  const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)hi, 1.0f, false);
+  const f16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)hi, 1.0f, true);
+  return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
 // Bytes of four words transposed: w[j] = byte j of t0, t1, t2, t3.
@@ -71,6 +85,9 @@ __device__ __forceinline__ void transpose4(uint32_t t0, uint32_t t1, uint32_t t2
 
 __device__ __forceinline__ f32x4 mfma(const bf16x8& a, const bf16x8& b, const f32x4& c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mfma(const f16x8& a, const f16x8& b, const f32x4& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
 // One request's queries and context, uniform over the wave.
@@ -192,26 +209,27 @@ __device__ __forceinline__ void load_v(const Kv8Cache& c, const Tile& x, int g, 
   }
 }
 
-// One row tile's probabilities (times the value's scale) of 32 tokens from
+// One row tile's probabilities, times the value's scale, of 32 tokens from
 // their raw scores; rescales l and o where the reference moves.
 template <int D>
-__device__ __forceinline__ bf16x8 probabilities(const f32x4 (&s)[2], const float (&ks)[2], const float (&lv)[2],
-                                                const float (&inv)[2], float& mref, float& l, f32x4 (&o)[D / 16]) {
+__device__ __forceinline__ f16x8 probabilities(const f32x4 (&s)[2], const float (&ks)[2], const float (&lv)[2],
+                                               const float (&inv)[2], float& mref, float& l, f32x4 (&o)[D / 16]) {
   float top[2];
 #pragma unroll
-  for (int u = 0; u < 2; ++u) top[u] = fmaxf(fmaxf(s[u][0], s[u][1]), fmaxf(s[u][2], s[u][3])) * ks[u];
+  for (int u = 0; u < 2; ++u)
+    top[u] = fmaf(fmaxf(fmaxf(s[u][0], s[u][1]), fmaxf(s[u][2], s[u][3])), ks[u], lv[u]);
   float t = fmaxf(top[0], top[1]);
-  if (__any(t > mref + kLazy)) {
+  if (__any(t > mref + kMost)) {
     t = fmaxf(t, __shfl_xor(t, 16));
     t = fmaxf(t, __shfl_xor(t, 32));
-    t = fmaxf(t, mref);
+    t = fmaxf(t - kFresh, mref);
     const float shrink = exp2f(mref - t);
     mref = t;
     l *= shrink;
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) o[j] *= shrink;
   }
-  bf16x8 p;
+  f16x8 p;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const float down = lv[u] - mref;
@@ -219,7 +237,7 @@ __device__ __forceinline__ bf16x8 probabilities(const f32x4 (&s)[2], const float
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       e[i] = __builtin_amdgcn_exp2f(fmaf(s[u][i], ks[u], down));
-      p[4 * u + i] = (__bf16)e[i];
+      p[4 * u + i] = (_Float16)e[i];
     }
     l = fmaf((e[0] + e[1]) + (e[2] + e[3]), inv[u], l);
   }
@@ -421,7 +439,7 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
             if (!now.x[u].ok || tok < see[t].lo || tok >= see[t].hi) s[t][u][i] = -INFINITY;
           }
     }
-    bf16x8 pv[MT];
+    f16x8 pv[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       pv[t] = probabilities<D>(s[t], now.ks, lv, inv, mref[t], l[t], o[t]);
@@ -435,7 +453,7 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
       transpose4(w.v[1][0][b], w.v[1][1][b], w.v[1][2][b], w.v[1][3][b], w1);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const bf16x8 v = cvt8(w0[j], w1[j]);
+        const f16x8 v = cvt8_f16(w0[j], w1[j]);
 #pragma unroll
         for (int t = 0; t < MT; ++t) o[t][4 * b + j] = mfma(v, pv[t], o[t][4 * b + j]);
       }

@@ -126,7 +126,7 @@ def masked_scores(q, K, there, kv, n, scale, causal, window):
 def attend(q, cu, kv_len, table, k_pool, v_pool, k_scale, v_scale, max_len, scale, causal=True, window=0):
     """(out, lse, tol_out, tol_lse) fp64.  Tolerances from the rounding count:
     scores are fp32 sums of D exact products (relative to sum |q k|), p is
-    rounded to bf16 once, the sums over L tokens are fp32, out is rounded to
+    rounded to fp16 once, the sums over L tokens are fp32, out is rounded to
     bf16."""
     N, Hq, D = q.shape
     H, B = k_pool.shape[1], k_pool.shape[2]
@@ -149,7 +149,7 @@ def attend(q, cu, kv_len, table, k_pool, v_pool, k_scale, v_scale, max_len, scal
         o = torch.einsum("hngl,hld->hngd", p, V)
         A = torch.einsum("hngl,hld->hngd", p, V.abs())
         d = (D + 8) * u * size.amax(-1) + 4 * u * s.masked_fill(s == -math.inf, 0).abs().amax(-1)     # of a score
-        tol = (2.0 ** -8 * (1 + 2.0 ** -6) + 2 * d[..., None] + (L + 64) * u) * A + 2.0 ** -8 * o.abs()
+        tol = (2.0 ** -11 * (1 + 2.0 ** -6) + 2 * d[..., None] + (L + 64) * u) * A + 2.0 ** -8 * o.abs()
         ls = top[..., 0] + torch.log(l)
         tl = d + (L + 64) * u + 4 * u * ls.abs().masked_fill(~some, 0.0)
         rows = lambda x: x.transpose(0, 1).reshape(n, Hq, *x.shape[3:])    # noqa: E731
