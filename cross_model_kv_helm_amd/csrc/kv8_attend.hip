@@ -209,6 +209,55 @@ __device__ __forceinline__ void load_v(const Kv8Cache& c, const Tile& x, int g, 
   }
 }
 
+// A value that is NaN reaches the rows that see its token and no other: where
+// the rows of a step see different tokens, 0 * NaN would reach them all.  Such a
+// step takes NaN codes as 0, and O becomes NaN where it has to after the loop.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t codes) {       // 1 in each byte that is one
+  return ((codes & 0x7f7f7f7fu) + 0x01010101u & 0x80808080u) >> 7;   // 0x7f carries into bit 7
+}
+template <int D>
+__device__ __forceinline__ bool holds_nan(const uint32_t (&v)[2][4][D / 64]) {
+  uint32_t any = 0;
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int b = 0; b < D / 64; ++b) any |= nan_bytes(v[u][i][b]);
+  return any != 0;
+}
+template <int D>
+__device__ __forceinline__ void drop_nan(uint32_t (&v)[2][4][D / 64]) {
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int b = 0; b < D / 64; ++b) v[u][i][b] &= ~(nan_bytes(v[u][i][b]) * 0xffu);
+}
+// O becomes NaN where the product of "is NaN" and "seen" is not 0.
+template <int D>
+__device__ __forceinline__ void put_nan(const uint32_t (&v)[2][4][D / 64], const f16x8& seen, f32x4 (&o)[D / 16]) {
+#pragma unroll
+  for (int b = 0; b < D / 64; ++b) {
+    uint32_t is[2][4], w0[4], w1[4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) is[u][i] = nan_bytes(v[u][i][b]) * 0x38u;   // the code of 1
+    transpose4(is[0][0], is[0][1], is[0][2], is[0][3], w0);
+    transpose4(is[1][0], is[1][1], is[1][2], is[1][3], w1);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const f32x4 hit = mfma(cvt8_f16(w0[j], w1[j]), seen, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        o[4 * b + j][i] = __uint_as_float(__float_as_uint(o[4 * b + j][i]) |
+                                          ((0u - min(__float_as_uint(hit[i]), 1u)) & 0x7fc00000u));
+    }
+  }
+}
+
 // One row tile's probabilities, times the value's scale, of 32 tokens from
 // their raw scores; rescales l and o where the reference moves.
 template <int D>
@@ -374,6 +423,7 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
 #pragma unroll
   for (int u = 0; u < 2; ++u) load_v<D>(c, now.x[u], g, m, w.v[u]);
 
+  bool met_nan = false;
   for (; t0 < end; t0 += kStride) {
     f32x4 s[MT][2];
     if constexpr (kWide) __builtin_amdgcn_s_setprio(1);
@@ -438,6 +488,8 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
             const int tok = t0 + 16 * u + 4 * g + i;
             if (!now.x[u].ok || tok < see[t].lo || tok >= see[t].hi) s[t][u][i] = -INFINITY;
           }
+      met_nan |= __any(holds_nan<D>(w.v));
+      drop_nan<D>(w.v);
     }
     f16x8 pv[MT];
 #pragma unroll
@@ -462,6 +514,27 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
     for (int u = 0; u < 2; ++u) load_v<D>(c, next.x[u], g, m, w.v[u]);
     if constexpr (kWide) __builtin_amdgcn_s_setprio(0);
     now = next;
+  }
+  if (met_nan) {
+    for (t0 = begin + tg * kStep; t0 < end; t0 += kStride) {
+      if (t0 >= s_last.lo && t0 + kStep <= s_first.hi) continue;      // NaN went its way in these
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        now.x[u] = tile_at(c, table, h, t0 + 16 * u, limit);
+        load_v<D>(c, now.x[u], g, m, w.v[u]);
+      }
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        f16x8 seen;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {      // by sign bits: conditions would take scalar registers by the dozen
+          const int tok = t0 + 16 * (e >> 2) + 4 * g + (e & 3);
+          const int out = (tok - see[t].lo) | (see[t].hi - 1 - tok) | (now.x[e >> 2].ok ? 0 : -1);
+          seen[e] = __builtin_bit_cast(_Float16, (uint16_t)(~(out >> 31) & 0x3c00));     // 1 or 0
+        }
+        put_nan<D>(w.v, seen, o[t]);
+      }
+    }
   }
 
   // join the waves of a row group: lane (g, m) has row m, d = g*D/4 + (D/16)*i + j

@@ -567,8 +567,8 @@ int helm_kv8_store(const void* k, const void* v, const int32_t* cu_seqlens, cons
  * Query head g attends KV head g / (n_q_heads / n_kv_heads).  A query that
  * sees nothing gives out = 0, lse = -inf.  Products are exact bf16 ones with
  * fp32 accumulation, statistics fp32; p is rounded to fp16 as the operand of
- * its product with V.  A NaN code inside a request's length spoils the
- * queries of its tile; codes past the length are never used.  The workspace
+ * its product with V.  A NaN code reaches the queries that see its token and
+ * no others; codes past the length are never used.  The workspace
  * (helm_kv8_attend_workspace_bytes, 256-byte aligned) holds the partial
  * results of a long context's pieces. */
 size_t helm_kv8_attend_workspace_bytes(const helm_kv8_shape_t* shape);

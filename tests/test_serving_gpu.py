@@ -348,6 +348,47 @@ def test_attend_absent_pages_and_lengths_past_the_bound(hk):
     within(w, want, tol, "absent weigh")
 
 
+@pytest.mark.parametrize("B,H,G,D,kv,new,window", [
+    (16, 1, 2, 128, [300], [100], 0), (32, 2, 5, 64, [90, 600], [40, 90], 0), (16, 1, 4, 128, [400, 50], [60, 50], 33),
+    (16, 2, 8, 128, [700], [4], 0), (32, 8, 5, 128, [300, 211, 70] * 4, [70, 70, 70] * 4, 0),
+    (16, 8, 8, 128, [1100], [1030], 0), (16, 2, 4, 128, [513], [1], 100)])
+def test_attend_nan_reaches_the_queries_that_see_it_and_no_others(hk, B, H, G, D, kv, new, window):
+    """NaN keys and values at a few tokens, of the prefix and among the new ones."""
+    c, q, cu = attend_inputs(B, H, G, D, kv, new, 55 + sum(kv))
+    clean = {n: t.clone() for n, t in c.items()}
+    bad_k, bad_v = torch.zeros(len(kv), max(kv), H, dtype=torch.bool), torch.zeros(len(kv), max(kv), H, D, dtype=torch.bool)
+    for r, (n, m) in enumerate(zip(kv, new)):
+        for i, t in enumerate({n - m // 2 - 1, n - 1 - m // 3, n - m, max(0, n - m - 7)}):
+            blk, h, d = int(c["table"][r, t // B]), i % H, (37 * i + r) % D
+            if i % 2:
+                c["v_pool"].view(torch.uint8)[blk, h, t % B, d] = 0xFF if i == 1 else 0x7F
+                bad_v[r, t, h, d] = True
+            else:
+                c["k_pool"].view(torch.uint8)[blk, h, t % B, d] = 0x7F
+                bad_k[r, t, h] = True
+            for x in ("k_pool", "v_pool"):      # the clean copy has numbers there
+                clean[x].view(torch.uint8)[blk, h, t % B, d] = 0
+                if x[0] != "kv"[i % 2]:
+                    c[x].view(torch.uint8)[blk, h, t % B, d] = 0
+    _, _, out, lse = run_attend(hk, c, q, cu, kv, True, window)
+    o, z, t_o, t_z = ref.attend(q, cu, kv, clean["table"], clean["k_pool"], clean["v_pool"], clean["k_scale"],
+                                clean["v_scale"], max(kv), D ** -0.5, True, window)
+    nan_o, nan_z = torch.zeros(o.shape, dtype=torch.bool), torch.zeros(z.shape, dtype=torch.bool)
+    for r, (n, m) in enumerate(zip(kv, new)):
+        for i in range(m):
+            p = n - m + i
+            seen = slice(max(0, p - window + 1) if window else 0, p + 1)
+            for h in range(H):
+                heads = slice(h * G, (h + 1) * G)
+                nan_z[cu[r] + i, heads] = bool(bad_k[r, seen, h].any())
+                nan_o[cu[r] + i, heads] = bad_v[r, seen, h].any(0) | bad_k[r, seen, h].any()
+    assert bool(nan_o.any())
+    assert torch.equal(out.cpu().isnan(), nan_o) and torch.equal(lse.cpu().isnan(), nan_z)
+    # a zeroed key code takes part in the clean scores: those rows are NaN here; the others agree with the clean result
+    within(out.cpu().double().masked_fill(nan_o, 0.0), o.masked_fill(nan_o, 0.0), t_o, "nan out")
+    within(lse.cpu().double().masked_fill(nan_z, 0.0), z.masked_fill(nan_z, 0.0), t_z, "nan lse")
+
+
 @pytest.mark.parametrize("new", [1, 50])
 def test_attend_peaked_scores_and_scales_of_any_size(hk, new):
     """Scores up to +-1e4 (the running maximum moves), scales that are no powers of two."""
