@@ -32,11 +32,11 @@
 //
 // Bounds and what was measured (one MI355X, 8 KV heads of 128): decode reads
 // 256 bytes a token and head and is bound by memory, 32 ragged requests of 273 K
-// tokens in 117 us with the join (4.7 TB/s), one of 131,072 tokens in 61 us.
+// tokens in 117 us with the join (4.7 TB/s), one of 131,072 tokens in 59 us.
 // Prompts are bound by issue: a 64 x 32 step of a wave is 1,024 cycles of
 // matrix work beside 1,600 of vector work (the codes' conversion, the softmax),
 // which overlap between two waves only in part; two requests of up to 2,048
-// tokens over 8,192, 40 query heads: 402 us, 857 TFLOP/s.
+// tokens over 8,192, 40 query heads: 415 us, 829 TFLOP/s.
 #include <math.h>
 
 #include "serve.hpp"
@@ -361,8 +361,8 @@ __device__ __forceinline__ void attend_stretch(const Kv8AttendArgs& a, const Req
 
   // Wide row tiles fill the registers with O: their queries wait in LDS, the
   // scheduler is kept from mixing the phases of a step (let loose it spilled 47
-  // registers, 748 us where this takes 437), and a wave in its matrix phases
-  // goes before one in its softmax (402 us).
+  // registers, 748 us for 437 at the prompt above), and a wave in its matrix
+  // phases goes before one in its softmax (437 -> 402).
   constexpr bool kWide = MT > 2;
   bf16x8 qv[kWide ? 1 : MT][KS];
   Seen see[MT];
