@@ -1,6 +1,7 @@
 // serve_entry.hip — the C entry points that serve over a transferred cache
 // (include/helm_kv.h, second part): host-side validation, workspace sizes and
 // dispatch.  Every check runs before anything is enqueued.
+#include <cfloat>
 #include <cmath>
 #include <new>
 #include <vector>
@@ -14,6 +15,7 @@ using namespace helm::entry;
 namespace {
 
 constexpr double kTwoPi = 6.283185307179586476925286766559;
+constexpr double kLog2e = 1.4426950408889634;
 constexpr int64_t kMaxContext = int64_t(1) << 30;
 
 struct Range {
@@ -128,6 +130,8 @@ int check_queries(const helm_kv8_shape_t* s) {
     return fail(HELM_E_INVALID_ARG, "window=%d must be >= 0, and 0 without causal", s->window);
   if (!std::isfinite(s->softmax_scale) || !(s->softmax_scale > 0.0))
     return fail(HELM_E_INVALID_ARG, "softmax_scale must be finite and > 0 (%g)", s->softmax_scale);
+  if (s->softmax_scale * kLog2e > FLT_MAX)      // the kernels hold the product in fp32
+    return fail(HELM_E_INVALID_ARG, "softmax_scale must be finite in fp32 times log2(e) (%g)", s->softmax_scale);
   if ((int64_t)s->n_requests * s->n_kv_heads > 0x7fffffffLL)
     return fail(HELM_E_INVALID_ARG, "n_requests * n_kv_heads exceeds 2^31-1");
   int64_t rows = s->n_tokens;
@@ -158,7 +162,7 @@ helm::Kv8AttendArgs attend_args(const helm_kv8_shape_t* s) {
   helm::group_magic_of((uint32_t)a.G, a.g_magic, a.g_shift);
   a.causal = s->causal;
   a.window = s->window;
-  a.scale_log2 = (float)(s->softmax_scale * 1.4426950408889634);
+  a.scale_log2 = (float)(s->softmax_scale * kLog2e);
   a.q_tok = s->tok_stride;
   a.q_head = s->head_stride;
   // no request can hold more than its table's pages

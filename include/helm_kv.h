@@ -538,7 +538,7 @@ typedef struct {
                               tokens past it, or past max_blocks * block_size, are absent */
   int64_t tok_stride, head_stride;       /* elements; of q (attend, weigh) or k (store) */
   int64_t v_tok_stride, v_head_stride;   /* of v (store) */
-  double softmax_scale;    /* finite, > 0 */
+  double softmax_scale;    /* > 0; times log2(e) finite in fp32 */
   void* stream;
   void* workspace;         /* helm_kv8_attend */
   size_t workspace_bytes;

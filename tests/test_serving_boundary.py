@@ -138,6 +138,13 @@ def test_query_shapes_refused(name, kw, status, text):
     refused(f(*FAR[:n], ctypes.byref(shape(**kw))), status, text)
 
 
+@pytest.mark.parametrize("name", ["attend", "weigh"])
+@pytest.mark.parametrize("scale", [3e38, 1e39, 1e308])
+def test_softmax_scale_past_fp32_refused(name, scale):
+    f, n = calls()[name]
+    refused(f(*FAR[:n], ctypes.byref(shape(softmax_scale=scale))), 1, "softmax_scale")
+
+
 def test_store_refusals():
     f, n = calls()["store"]
     refused(f(*FAR[:n], ctypes.byref(shape(dtype=2))), 5, "dtype")
