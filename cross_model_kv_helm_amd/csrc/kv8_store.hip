@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kThreads) kv8_store_kernel(Kv8StoreArgs a) {
     const int64_t slab = (int64_t)blk * c.H + h;
     uint8_t* pool = (is_v ? c.v_pool : c.k_pool) + slab * c.B * c.D;
     float* scale = (is_v ? c.v_scale : c.k_scale) + slab;
-    const float was = o0 > 0 ? *scale : 0.0f;
+    const float was = o0 > 0 ? fmaxf(*scale, 0.0f) : 0.0f;   // NaN and negative: no scale, codes that stand for 0
 
     Piece<T> x[U];
     float amax = 0.0f;
@@ -96,14 +96,14 @@ __global__ void __launch_bounds__(kThreads) kv8_store_kernel(Kv8StoreArgs a) {
     }
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
-    const float now = fmaxf(kv8_scale_of(amax), was);   // fmaxf: a NaN scale counts as none
+    const float now = fmaxf(kv8_scale_of(amax), was);
     const float inv = 1.0f / now;                       // exact for a power of two
     if (lane == 0) *scale = now;
     if (o0 > 0 && was != now) {
       const float ratio = was * inv;
       for (int u = lane; u < o0 * (c.D / 4); u += 64) {
         uint32_t* p = (uint32_t*)pool + u;
-        const f32x4 y = kv8_decode4(*p);
+        const f32x4 y = kv8_decode4(was > 0.0f ? *p : 0u);
         *p = kv8_encode4(y[0] * ratio, y[1] * ratio, y[2] * ratio, y[3] * ratio);
       }
     }

@@ -549,7 +549,8 @@ typedef struct {
  * kv_start[r] + i.
  * A block that held tokens of its request before (kv_start inside it) keeps
  * the larger of its scale and the one the new tokens need; where that grows
- * it, the tokens held are re-coded.  Codes round to nearest even; infinities
+ * it, the tokens held are re-coded (a scale that is NaN or not above 0 is
+ * none: what it scaled counts as 0).  Codes round to nearest even; infinities
  * saturate to +-448 and do not count in max|x|; NaN stays NaN.
  *   cu_seqlens : [R+1] int32;  kv_start : [R] int32, >= 0
  *   weights    : NULL, or the accumulated weights, set to 0 for stored tokens

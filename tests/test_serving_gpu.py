@@ -211,6 +211,27 @@ def test_store_odd_values(hk):
         assert torch.equal(a.isnan(), b.isnan()) and torch.equal(a.nan_to_num(), b.nan_to_num()), n
 
 
+@pytest.mark.parametrize("was", [math.nan, -0.5, 0.0])
+def test_store_behind_codes_without_a_scale(hk, was):
+    """Codes whose block has no scale stand for 0, NaN codes too: they are 0 once it has one."""
+    B, H, D = 32, 2, 64
+    c = ref.cache(gen_of(31), [20], B, H, D)
+    c["table"][:] = 0
+    for n in ("k", "v"):
+        c[n + "_pool"].view(torch.uint8)[0] = torch.randint(0, 256, (H, B, D), generator=gen_of(32), dtype=torch.uint8)
+        c[n + "_scale"][0] = was
+    x = torch.randn((9, H, D), generator=gen_of(33)).to(torch.bfloat16)
+    d, _ = run_store(hk, c, [x, x], [0, 9], [11], 20)
+    e = ref.cache(gen_of(31), [20], B, H, D)
+    e["table"][:] = 0
+    ref.store(x, e["k_pool"], e["k_scale"], [0, 9], [0], e["table"], 20)      # the new tokens by themselves
+    for n in ("k", "v"):
+        assert same_bits(d[n + "_scale"][0], e["k_scale"][0])
+        codes = d[n + "_pool"][0].cpu().view(torch.uint8)
+        assert bool((codes[:, :11] == 0).all())
+        assert torch.equal(codes[:, 11:20], e["k_pool"][0].view(torch.uint8)[:, :9])
+
+
 def test_store_in_steps_agrees_with_one_call(hk):
     """Power-of-two scales: a block grown token by token holds what one call gives, but for codes below
     e4m3's normal range, which round twice."""
