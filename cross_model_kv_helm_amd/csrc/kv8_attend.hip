@@ -36,7 +36,7 @@
 // Prompts are bound by issue: a 64 x 32 step of a wave is 1,024 cycles of
 // matrix work beside 1,600 of vector work (the codes' conversion, the softmax),
 // which overlap between two waves only in part; two requests of up to 2,048
-// tokens over 8,192, 40 query heads: 415 us, 829 TFLOP/s.
+// tokens over 8,192, 40 query heads: 407 us, 846 TFLOP/s.
 #include <math.h>
 
 #include "serve.hpp"
@@ -258,6 +258,11 @@ __device__ __forceinline__ void put_nan(const uint32_t (&v)[2][4][D / 64], const
   }
 }
 
+// The larger, NaN if either is (such a row is NaN anyway).  Unlike fmaxf's it is
+// one instruction for three numbers and takes the matrix unit's results as they
+// are, 10 instructions fewer a row tile: 413 -> 407 us at the prompt above.
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 // One row tile's probabilities, times the value's scale, of 32 tokens from
 // their raw scores; rescales l and o where the reference moves.
 template <int D>
@@ -266,7 +271,7 @@ __device__ __forceinline__ f16x8 probabilities(const f32x4 (&s)[2], const float 
   float top[2];
 #pragma unroll
   for (int u = 0; u < 2; ++u)
-    top[u] = fmaf(fmaxf(fmaxf(s[u][0], s[u][1]), fmaxf(s[u][2], s[u][3])), ks[u], lv[u]);
+    top[u] = fmaf(larger(larger(larger(s[u][0], s[u][1]), s[u][2]), s[u][3]), ks[u], lv[u]);
   float t = fmaxf(top[0], top[1]);
   if (__any(t > mref + kMost)) {
     t = fmaxf(t, __shfl_xor(t, 16));
