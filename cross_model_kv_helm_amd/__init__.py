@@ -569,19 +569,27 @@ def _bind_serving(L):
 # each tensor once, and the messages are made only for a tensor that fails.
 def _ptr(t, name, dtype, shape):
     """Address of a contiguous GPU tensor of this type and shape."""
-    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:      # no tensor
+        pass
     return _dev_ptr(t, name, dtype, shape)
 
 
-def _heads_ptr(t, name, dtype, shape):
-    """Address of a [tokens, heads, dim] GPU tensor of any token and head
-    strides whose heads are contiguous; the two strides come back with it."""
+def _on_gpu(t, name):
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must live on the GPU (got {t.device})")
+    return t
+
+
+def _heads_ptr(t, name, dtype, shape):
+    """Address of a [tokens, heads, dim] GPU tensor of any token and head
+    strides whose heads are contiguous; the two strides come back with it."""
+    _on_gpu(t, name)
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
     if t.shape != shape:
@@ -599,10 +607,10 @@ def _stream_of(t):
 
 
 def _serving_shape(shape, t):
-    """A copy of the caller's shape for one call, its stream resolved as in _call_shape."""
+    """A copy of the caller's shape for one call on pool t, its stream resolved as in _call_shape."""
     s = type(shape).from_buffer_copy(shape)
     if not s.stream:
-        s.stream = _stream_of(t)
+        s.stream = _stream_of(_on_gpu(t, "k_pool"))
     return s
 
 
@@ -638,7 +646,7 @@ def helm_rope(q, k, pos, rope: HelmRope, mode: int = HELM_ROPE_FORWARD, out_q=No
     x = q if q is not None else k
     if x is None:
         raise ValueError("q or k must be given")
-    N, _, D = x.shape
+    N, _, D = _on_gpu(x, "q" if q is not None else "k").shape
     dt = x.dtype
     s = HelmRopeShape(0, 0, _dtype_code(x), mode, N)
     if D != rope.head_dim:
@@ -702,7 +710,7 @@ def helm_kv8_store(k, v, cu_seqlens, kv_start, block_table, k_pool, v_pool, k_sc
     strides) into the 8-bit cache, behind each request's kv_start tokens.
     ``weights``: the accumulated weights, zeroed for the stored tokens."""
     s = _serving_shape(shape, k_pool)
-    s.dtype = _dtype_code(k)
+    s.dtype = _dtype_code(_on_gpu(k, "k"))
     nhd = (s.n_tokens, s.n_kv_heads, s.head_dim)
     kp, s.tok_stride, s.head_stride = _heads_ptr(k, "k", k.dtype, nhd)
     vp, s.v_tok_stride, s.v_head_stride = _heads_ptr(v, "v", k.dtype, nhd)

@@ -266,3 +266,28 @@ def test_binding_checks():
         hk._heads_ptr(t, "q", torch.bfloat16, (2, 3, 64))
     with pytest.raises(ValueError, match="q or k"):
         hk.helm_rope(None, None, None, hk.make_rope(64, 1e6))
+
+
+@pytest.mark.parametrize("bad", [None, 3, "cpu"])
+@pytest.mark.parametrize("name,at", [("store", 0), ("store", 2), ("store", 5), ("attend", 0), ("attend", 1), ("attend", 4),
+                                     ("weigh", 1), ("weigh", 5), ("evict", 0), ("evict", 4), ("rope", 0), ("rope", 2)])
+def test_python_arguments_are_named(name, at, bad):
+    """What is no tensor, or none on a GPU, is refused by name before the stream is asked for."""
+    torch = pytest.importorskip("torch")
+
+    def some(dtype, *dims):
+        return torch.zeros(dims, dtype=dtype)
+    bf, f32, i32, f8 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
+    pool, scale, table = some(f32, 4, 2, 16, 64).to(f8), some(f32, 4, 2), some(i32, 1, 4)
+    q, cu, n, w, lse = some(bf, 1, 2, 64), some(i32, 2), some(i32, 1), some(f32, 4, 2, 16), some(f32, 1, 2)
+    s, e = hk.make_kv8_shape(pool, table, 1, n_q_heads=2), hk.make_kv8_evict_shape(pool, table, table, 4, 1)
+    f, args = {"store": (hk.helm_kv8_store, [q, q, cu, n, table, pool, pool, scale, scale, s]),
+               "attend": (hk.helm_kv8_attend, [q, cu, n, table, pool, pool, scale, scale, s]),
+               "weigh": (hk.helm_kv8_weigh, [q, lse, cu, n, table, pool, scale, w, s]),
+               "evict": (hk.helm_kv8_evict, [w, n, table, table, pool, pool, scale, scale, e]),
+               "rope": (hk.helm_rope, [q, None, cu[:1], hk.make_rope(64, 1e4)])}[name]
+    if bad != "cpu":
+        args[at] = bad
+    what = "q or k must be given" if name == "rope" and at == 0 and bad is None else "must be a torch tensor|must live on the GPU"
+    with pytest.raises((TypeError, ValueError), match=what):
+        f(*args)
