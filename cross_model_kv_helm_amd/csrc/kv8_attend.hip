@@ -873,8 +873,12 @@ __device__ __forceinline__ void convert_k(const u32x4 (&w)[D / 64], bf16x8 (&k)[
 }
 
 // Few rows: a wave streams through its stretch of the context, 32 tokens at a
-// time with the next keys in flight, the first row tile in registers.
-template <int D>
+// time with the next keys in flight, the first row tile in registers.  ONE: as a
+// rule there is no other, and what others there are take its place in turn,
+// which leaves registers for a fourth wave a SIMD: 32 ragged requests of one
+// token, 8 heads a group, 65 us for 72.  Where there are others the room for
+// two is worth more: 4 tokens over 8,192, 16 requests, 38 us for 50.
+template <int D, bool ONE>
 __device__ __forceinline__ void weigh_stretch(const Kv8AttendArgs& a, const Request& q, int h, int from, int to) {
   const Kv8Cache& c = a.c;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -885,7 +889,7 @@ __device__ __forceinline__ void weigh_stretch(const Kv8AttendArgs& a, const Requ
   float lse[4];
   load_rows<D, false>(a, q, h, 0, g, m, rows);
   row_lse(rows.lse, m < M, g, lse);
-  const Seen s_first = seen_by(a, q, 0), s_last = seen_by(a, q, query_of(a, min(16, M) - 1));
+  const Seen s_first = seen_by(a, q, 0), s_last = seen_by(a, q, ONE ? q.n - 1 : query_of(a, min(16, M) - 1));
   int t0 = from + wave * kStep;
   Tile now[2], next[2];
   u32x4 kw[2][D / 64];
@@ -919,13 +923,23 @@ __device__ __forceinline__ void weigh_stretch(const Kv8AttendArgs& a, const Requ
     const bool own = g < 2 && mine.ok && tok < to;
     if (own) was = *w;
     float acc[2] = {0.0f, 0.0f};
-    add_weights<D, 2>(a, q, rows.q, k, scale, lse, 4 * g, t0 >= s_last.lo && t0 + kStep <= s_first.hi, t0 + m, acc);
-    for (int row0 = 16; row0 < M; row0 += 16) {
-      RowTile<D> x;
-      float z[4];
-      load_rows<D, false>(a, q, h, row0, g, m, x);
-      row_lse(x.lse, row0 + m < M, g, z);
-      add_weights<D, 2>(a, q, x.q, k, scale, z, row0 + 4 * g, false, t0 + m, acc);
+    const bool all = t0 >= s_last.lo && t0 + kStep <= s_first.hi;
+    if constexpr (ONE) {
+#pragma unroll 1
+      for (int row0 = 0; row0 < M; row0 += 16) {
+        if (M > 16) row_lse(rows.lse, row0 + m < M, g, lse);
+        add_weights<D, 2>(a, q, rows.q, k, scale, lse, row0 + 4 * g, all, t0 + m, acc);
+        if (M > 16) load_rows<D, false>(a, q, h, row0 + 16 < M ? row0 + 16 : 0, g, m, rows);
+      }
+    } else {
+      add_weights<D, 2>(a, q, rows.q, k, scale, lse, 4 * g, all, t0 + m, acc);
+      for (int row0 = 16; row0 < M; row0 += 16) {
+        RowTile<D> x;
+        float z[4];
+        load_rows<D, false>(a, q, h, row0, g, m, x);
+        row_lse(x.lse, row0 + m < M, g, z);
+        add_weights<D, 2>(a, q, x.q, k, scale, z, row0 + 4 * g, false, t0 + m, acc);
+      }
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -942,17 +956,17 @@ __device__ __forceinline__ void weigh_stretch(const Kv8AttendArgs& a, const Requ
 template <int D>
 __global__ void __launch_bounds__(kThreads, 3) kv8_weigh_kernel(Kv8AttendArgs a) {
   const Request q = request_at(a, blockIdx.x / a.c.H);
-  if (q.n > 0) weigh_stretch<D>(a, q, blockIdx.x % a.c.H, from_of(a, q), q.len);
+  if (q.n > 0) weigh_stretch<D, false>(a, q, blockIdx.x % a.c.H, from_of(a, q), q.len);
 }
 // One workgroup, one piece of the division (whose items have all rows).
-template <int D>
-__global__ void __launch_bounds__(kThreads, 3) kv8_weigh_pieces_kernel(Kv8AttendArgs a) {
+template <int D, bool ONE>
+__global__ void __launch_bounds__(kThreads, ONE ? 4 : 3) kv8_weigh_pieces_kernel(Kv8AttendArgs a) {
   Division d;
   if (!division_at(a, blockIdx.x, d)) return;
   const int in = (int)blockIdx.x - d.first, item = in / d.pieces, part = in - item * d.pieces;
   if (item >= d.items) return;
   const int per = (d.units + d.pieces - 1) / d.pieces * kUnit, from = d.from + part * per;
-  weigh_stretch<D>(a, d.q, item, from, min(d.q.len, from + per));
+  weigh_stretch<D, ONE>(a, d.q, item, from, min(d.q.len, from + per));
 }
 
 // Many rows (prompts): NW waves share 16*SUB tokens, whose keys stay in registers,
@@ -1067,6 +1081,9 @@ hipError_t attend(const Kv8AttendArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// The requests have 16 rows or fewer, on average.
+bool one_row_tile(const Kv8AttendArgs& a) { return a.n_tok * a.G <= 16 * (int64_t)a.c.R; }
+
 template <int D>
 hipError_t weigh(const Kv8AttendArgs& a, hipStream_t stream) {
   if (a.n_tok * a.G > 64 * (int64_t)a.c.R) {
@@ -1077,8 +1094,10 @@ hipError_t weigh(const Kv8AttendArgs& a, hipStream_t stream) {
       kv8_weigh_rows_kernel<D, 8, 8><<<grid(128), 512, 0, stream>>>(a);
     else
       kv8_weigh_rows_kernel<D, 4, 4><<<grid(64), 256, 0, stream>>>(a);
+  } else if (a.pieces && one_row_tile(a)) {
+    kv8_weigh_pieces_kernel<D, true><<<dim3((unsigned)a.pieces), kThreads, 0, stream>>>(a);
   } else if (a.pieces) {
-    kv8_weigh_pieces_kernel<D><<<dim3((unsigned)a.pieces), kThreads, 0, stream>>>(a);
+    kv8_weigh_pieces_kernel<D, false><<<dim3((unsigned)a.pieces), kThreads, 0, stream>>>(a);
   } else {
     kv8_weigh_kernel<D><<<dim3((unsigned)(a.c.R * a.c.H)), kThreads, 0, stream>>>(a);
   }
@@ -1087,9 +1106,10 @@ hipError_t weigh(const Kv8AttendArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-// Three workgroups a CU are resident with 16 rows (two with 32).  One round of
-// equal pieces beat both fewer and more: 32 ragged requests 117 us with 768,
-// 144 with 512, 129 with 1,536; a 131,072-token context 61, 63 and 67 us.
+// Pieces of 16 rows that fill the chip: three workgroups a CU (two with 32 rows),
+// though the registers have room for four.  32 ragged requests, and one context of
+// 131,072 tokens: 117 and 59 us with 768, 115 and 62 with 1,024, 120 and 61 with
+// 704, 120 and 63 with 1,280.
 constexpr int64_t kFill = 768;
 
 // Pieces for `items` items (at most `most`), in whose contexts the queries see
@@ -1109,7 +1129,7 @@ static void divide(Kv8AttendArgs& a, int64_t items, int64_t most, int64_t fill) 
 
 void kv8_attend_plan(Kv8AttendArgs& a) {
   const int64_t rows = a.n_tok * a.G, R = a.c.R;
-  a.row_tile = rows <= 16 * R ? 16 : 32;
+  a.row_tile = one_row_tile(a) ? 16 : 32;
   const int64_t some = R < a.n_tok ? R : a.n_tok;      // requests with queries, at most
   const int64_t full = (rows + a.row_tile - 1) / a.row_tile, most = rows / a.row_tile + R;
   divide(a, (full < some ? some : full) * a.c.H, (most < rows ? most : rows) * a.c.H, a.row_tile == 16 ? kFill : kFill * 2 / 3);
@@ -1127,7 +1147,8 @@ void kv8_attend_plan(Kv8AttendArgs& a) {
 void kv8_weigh_plan(Kv8AttendArgs& a) {
   const int64_t some = a.c.R < a.n_tok ? a.c.R : a.n_tok;
   a.row_tile = 0x7fffffff;     // an item has all rows of a request and head
-  divide(a, some * a.c.H, some * a.c.H, kFill);
+  // four workgroups a CU, or three, as the registers allow (768 of the four: 74 us for 65)
+  divide(a, some * a.c.H, some * a.c.H, one_row_tile(a) ? kFill * 4 / 3 : kFill);
 }
 
 size_t kv8_attend_workspace(const Kv8AttendArgs& a) {

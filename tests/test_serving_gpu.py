@@ -322,6 +322,15 @@ def test_attend_and_weigh(hk, B, H, G, D, kv, new, causal, window):
     within(w, 2 * once - w0.double(), 2 * tol, "weigh")
 
 
+@pytest.mark.parametrize("B,H,G,D,kv,new,causal,window", [
+    (16, 2, 8, 128, [2500, 1800, 300, 900], [5, 1, 1, 1], True, 0),
+    (32, 1, 5, 64, [4000, 33, 1, 2100], [7, 3, 1, 1], True, 700),
+    (48, 2, 3, 128, [60, 3100, 0, 1500, 17], [0, 16, 0, 2, 1], False, 0)])
+def test_many_rows_of_one_request_among_single_tokens(hk, B, H, G, D, kv, new, causal, window):
+    """Few rows on average, but several row tiles in one of the requests, whose context is cut into pieces."""
+    test_attend_and_weigh(hk, B, H, G, D, kv, new, causal, window)
+
+
 @pytest.mark.parametrize("D", [64, 128])
 def test_attend_strided_queries_on_another_stream(hk, D):
     B, H, G, kv, new = 16, 2, 3, [200, 77], [3, 1]
