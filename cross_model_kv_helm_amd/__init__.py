@@ -578,12 +578,12 @@ def _ptr(t, name, dtype, shape):
 
 
 def _on_gpu(t, name):
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must live on the GPU (got {t.device})")
-    return t
+    try:
+        if t.is_cuda:
+            return t
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch tensor") from None
+    raise ValueError(f"{name} must live on the GPU (got {t.device})")
 
 
 def _heads_ptr(t, name, dtype, shape):
