@@ -10,16 +10,17 @@
 // The keys are held in LDS where they fit (contexts up to 36,448 tokens), so
 // the weights are read once; else every pass reads them again.  The histogram
 // has 16 copies, one for every 16th lane, so that at most four lanes meet in an
-// atomic.  16 requests of up to 32,768 tokens, 8 heads: 39 us, bound by the
-// barriers and LDS work of 128 workgroups, not by memory.  Four digits counted
-// from the sign on had taken 16 us, indices with counts passed by shuffles 12.
+// atomic.  16 requests of up to 32,768 tokens, 8 heads: 31 us, bound by the
+// vector and LDS work of 128 workgroups, not by memory.  Of 38 us the reading
+// took 11 before its loads went side by side, the digits 15 and the indices 8,
+// whose counts are summed over the lanes by moves between registers.
 //
 // Copy, one wave per (block written, head): the kept tokens' codes, whose
 // blocks have scales of their own, are taken to one new scale, K and V side by
 // side from one look at the indices and the table.  A block's codes stay in
 // registers between finding their size and writing them.  The blocks written
 // are disjoint from the blocks read, so the copies need no order.  Bound by
-// memory: 2 bytes moved per kept value, 8 per token looked at: 64 us
+// memory: 2 bytes moved per kept value, 8 per token looked at: 63 us
 // for those 16 requests, 4.2 TB/s.
 #include "serve.hpp"
 
@@ -29,6 +30,7 @@ namespace {
 constexpr int kSelThreads = 1024;
 constexpr int kSelWaves = kSelThreads / 64;
 constexpr int kCopies = 16;
+constexpr int kAhead = 4;                // 8 took 1 us longer
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kKeysInLds = 36448;        // with the histogram just under 160 KB
@@ -59,6 +61,18 @@ __device__ __forceinline__ u32x4 keys_at(const Kv8EvictArgs& a, const int32_t* r
   return u32x4{key_of(w[0]), key_of(w[1]), key_of(w[2]), key_of(w[3])};
 }
 
+// The sum of x over this lane and those before it, within the registers: rows of
+// 16 lanes first, then the row before, then the half before.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x111, 0xf, 0xf, true);     // from 1 lane below
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x112, 0xf, 0xf, true);     // 2
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x114, 0xf, 0xf, true);     // 4
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x118, 0xf, 0xf, true);     // 8
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x142, 0xa, 0xf, false);    // row 0's last to row 1, 2's to 3
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x143, 0xc, 0xf, false);    // lane 31's to rows 2 and 3
+  return x;
+}
+
 template <bool LDS>
 __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(Kv8EvictArgs a) {
   extern __shared__ uint32_t keys[];
@@ -84,16 +98,35 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(Kv8EvictArgs a)
 
   const auto four = [&](int t) { return LDS ? *(const u32x4*)&keys[t] : keys_at(a, row, h, t); };
   uint32_t least = ~0u, most = 0u;
-#pragma unroll 4
-  for (int t = 4 * tid; t < cand; t += 4 * kSelThreads) {
-    const u32x4 k = keys_at(a, row, h, t);
-    if constexpr (LDS) *(u32x4*)&keys[t] = k;
+  // kAhead loads of a thread in flight, of the table and then of the weights: no
+  // branch stands between them (one read at a time took 11 us of 38)
+  for (int base = 4 * tid; base < cand; base += kAhead * 4 * kSelThreads) {
+    const float* w[kAhead];
+    f32x4 x[kAhead];
+    bool ok[kAhead];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (t + i < cand) {
-        least = min(least, k[i]);
-        most = max(most, k[i]);
-      }
+    for (int j = 0; j < kAhead; ++j) {
+      const int t = min(base + j * 4 * kSelThreads, (cand - 1) & ~3), page = page_of(c, t), blk = row[page];
+      ok[j] = (uint32_t)blk < (uint32_t)c.n_blocks;
+      w[j] = a.weights + ((int64_t)(ok[j] ? blk : 0) * c.H + h) * c.B + (t - page * c.B);
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) __builtin_memcpy(&x[j], w[j], 16);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int t = base + j * 4 * kSelThreads;
+      if (t >= cand) break;
+      u32x4 k;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) k[i] = ok[j] ? key_of(x[j][i]) : 0u;
+      if constexpr (LDS) *(u32x4*)&keys[t] = k;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (t + i < cand) {
+          least = min(least, k[i]);
+          most = max(most, k[i]);
+        }
+    }
   }
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) {
@@ -121,9 +154,15 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(Kv8EvictArgs a)
     int* mine = hist + (lane & (kCopies - 1));
     for (int t = 4 * tid; t < cand; t += 4 * kSelThreads) {
       const u32x4 k = four(t);
+      if (t + 4 <= cand) {               // all but the last ones: nothing to compare with the end
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (((k[i] ^ prefix) & mask) == 0 && t + i < cand) atomicAdd(&mine[((k[i] >> shift) & digits) * kCopies], 1);
+        for (int i = 0; i < 4; ++i)
+          if (((k[i] ^ prefix) & mask) == 0) atomicAdd(&mine[((k[i] >> shift) & digits) * kCopies], 1);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          if (((k[i] ^ prefix) & mask) == 0 && t + i < cand) atomicAdd(&mine[((k[i] >> shift) & digits) * kCopies], 1);
+      }
     }
     __syncthreads();
     if (tid < 256) {
@@ -193,19 +232,28 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(Kv8EvictArgs a)
   // each wave's stretch of the tokens: first what it holds, then where it goes
   const int per = (n + kSelThreads * 4 - 1) / (kSelThreads * 4) * 256;
   const int t0 = min(wave * per, n), t1 = min(t0 + per, n);
-  const uint64_t bound = need > 0 ? prefix : uint64_t(1) << 32;      // above every key where none competes
+  const uint32_t bound = need > 0 ? prefix : ~0u;      // where none competes: no weight has this key
   const auto kind = [&](int t, u32x4 k, int i) {       // 2: above, 1: equal, 0: neither
     const int x = k[i] > bound ? 2 : k[i] == bound ? 1 : 0;
     return t + i >= t1 ? 0 : t + i >= cand ? 2 : x;
   };
+  const int inner = min(t1, cand);         // before it both bounds of kind() hold
   int over = 0, ties = 0;
   for (int t = t0 + 4 * lane; t < t1; t += 256) {
     const u32x4 k = t < cand ? four(t) : u32x4{0, 0, 0, 0};
+    if (t + 4 <= inner) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int x = kind(t, k, i);
-      over += x == 2;
-      ties += x == 1;
+      for (int i = 0; i < 4; ++i) {
+        over += k[i] > bound;
+        ties += k[i] == bound;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int x = kind(t, k, i);
+        over += x == 2;
+        ties += x == 1;
+      }
     }
   }
 #pragma unroll
@@ -227,22 +275,33 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(Kv8EvictArgs a)
   for (int t = t0; t < t1; t += 256) {     // all lanes stay in the loop: they exchange counts
     const int mine = t + 4 * lane;
     const u32x4 k = mine < cand ? four(mine) : u32x4{0, 0, 0, 0};
-    int x[4], at_o = 0, at_e = same, all_o = 0, all_e = 0;   // above and equal: before this lane's, in all
+    bool more[4], even[4];
+    uint32_t own = 0;                      // above, and equal in the upper half
+    if (t + 256 <= inner) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i] = kind(mine, k, i);
-      const uint64_t o = __ballot(x[i] == 2), e = __ballot(x[i] == 1);
-      at_o += __builtin_amdgcn_mbcnt_hi((uint32_t)(o >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)o, 0));
-      at_e += __builtin_amdgcn_mbcnt_hi((uint32_t)(e >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)e, 0));
-      all_o += __popcll(o);
-      all_e += __popcll(e);
+      for (int i = 0; i < 4; ++i) {
+        more[i] = k[i] > bound;
+        even[i] = k[i] == bound;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int x = kind(mine, k, i);
+        more[i] = x == 2;
+        even[i] = x == 1;
+      }
     }
 #pragma unroll
+    for (int i = 0; i < 4; ++i) own += (more[i] ? 1u : 0u) + (even[i] ? 0x10000u : 0u);
+    const uint32_t upto = wave_scan(own), all = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63), here = upto - own;
+    int at_o = (int)(here & 0xffffu), at_e = same + (int)(here >> 16);
+    const int all_o = (int)(all & 0xffffu), all_e = (int)(all >> 16);
+    const int gone = min(same, need);
+#pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (x[i] == 2 || (x[i] == 1 && at_e < need))
-        kept[written + at_o + (min(at_e, need) - min(same, need))] = mine + i;
-      at_o += x[i] == 2;
-      at_e += x[i] == 1;
+      if (more[i] || (even[i] && at_e < need)) kept[written + at_o + (min(at_e, need) - gone)] = mine + i;
+      at_o += more[i];
+      at_e += even[i];
     }
     written += all_o + (min(same + all_e, need) - min(same, need));
     same += all_e;
@@ -270,34 +329,34 @@ __global__ void __launch_bounds__(kThreads) kv8_copy_kernel(Kv8EvictArgs a) {
 
   u32x4 k[U], v[U];
   float ks[U], vs[U], wt[U], k_max = 0.0f, v_max = 0.0f;
+  // no branch stands between the loads, which wait for each other as it is: a
+  // token that is not there reads the first block's and is set to 0 then
   const auto load = [&](int u0) {
     int64_t from[U];
     int off[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int u = u0 + i * 64 + lane, j = u >> shift;
-      from[i] = -1;
-      off[i] = 0;
-      if (u < all && j < cnt) {
-        const int t = min((uint32_t)kept[j], (uint32_t)n - 1u), sp = page_of(c, t), sb = row[sp];
-        off[i] = t - sp * c.B;
-        if ((uint32_t)sb < (uint32_t)c.n_blocks) from[i] = (int64_t)sb * c.H + h;
-      }
+      const int j = (u0 + i * 64 + lane) >> shift;     // below cnt <= B: inside the block as well
+      const int t = min((uint32_t)kept[min(j, cnt - 1)], (uint32_t)n - 1u), sp = page_of(c, t), sb = row[sp];
+      off[i] = t - sp * c.B;
+      from[i] = j < cnt && (uint32_t)sb < (uint32_t)c.n_blocks ? (int64_t)sb * c.H + h : -1;
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int part = lane & (per - 1);               // 64 is a multiple of a token's pieces
-      k[i] = v[i] = u32x4{0, 0, 0, 0};
-      ks[i] = vs[i] = wt[i] = 0.0f;
-      if (from[i] >= 0) {
-        const int64_t slot = from[i] * c.B + off[i];
-        k[i] = *(const u32x4*)(c.k_pool + slot * c.D + part * 16);
-        v[i] = *(const u32x4*)(c.v_pool + slot * c.D + part * 16);
-        ks[i] = c.k_scale[from[i]];
-        vs[i] = c.v_scale[from[i]];
-        if (part == 0) wt[i] = a.weights[slot];
-      }
+      const int64_t slab = max(from[i], (int64_t)0), slot = slab * c.B + off[i];
+      k[i] = *(const u32x4*)(c.k_pool + slot * c.D + part * 16);
+      v[i] = *(const u32x4*)(c.v_pool + slot * c.D + part * 16);
+      ks[i] = c.k_scale[slab];
+      vs[i] = c.v_scale[slab];
+      wt[i] = part == 0 ? a.weights[slot] : 0.0f;
     }
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (from[i] < 0) {
+        k[i] = v[i] = u32x4{0, 0, 0, 0};
+        ks[i] = vs[i] = wt[i] = 0.0f;
+      }
   };
   const auto size = [&]() {
 #pragma unroll
